@@ -449,6 +449,103 @@ vsd_status vsd_spec_loop(const vsd_model* target, const vsd_model* drafter, vsd_
  * (request b: the residual row of its last accepted position) to dst_dev. */
 vsd_status vsd_kv_get_anchor(const vsd_kv* kv, int32_t batch, float* dst_dev, vsd_stream stream);
 
+/* ---------------------------------------------------------------- single-token serving
+ * What a request needs next to block verification when one token at a time is
+ * produced: attention of its new token over the same paged cache, a cache that
+ * can be cut to a budget of rows, and a token drawn from a row of logits.
+ * Asynchronous; no allocation, no workspace of the cache is used, so calls may
+ * be captured in CUDA graphs, and calls on different streams may overlap as
+ * long as they touch different requests' rows.  Pointers belong to the device
+ * that is current, which must be the cache's. */
+
+/* Device addresses of the cache's K and V pools, BF16
+ * [layers][num_pages][n_kv][16][head_dim] (row i of request b: page-table
+ * entry i / 16 of b, row i % 16 of that page), owned by the cache and valid
+ * until it is destroyed. */
+vsd_status vsd_kv_pools(const vsd_kv* kv, uint16_t** k_dev, uint16_t** v_dev);
+
+/* Attention of one new token per request over layer `layer` of the cache.
+ *   seq_lens_dev int32 [B]: cached rows L_b, not changed (-1: idle slot)
+ *   q_dev   BF16 [B, n_q, hd], RoPE already applied
+ *   k_new_dev, v_new_dev BF16 [B, n_kv, hd]: the new token's rows (RoPE
+ *           applied to K); they are attended to and written to cache row L_b.
+ *           Both NULL: the cached rows alone (a cache of fixed keys, such as
+ *           an encoder's).
+ *   window  0: all rows; else only the last `window` of them, the new row
+ *           among them
+ *   score_dev optional float32 [B, n_kv, max_tokens_per_req]: for each row i
+ *           attended to, the weights p_i of the KV head's query heads are
+ *           added to entry i (the new row's entry is set, not added to)
+ *   out_dev f16 [B, n_q * hd];  lse_dev optional float32 [B, n_q]: the natural
+ *           logarithm of the sum of exp(score)
+ * With n = L_b + 1 (L_b without new rows) and scores q.K_i / sqrt(hd), the
+ * rows max(0, n - window) .. n - 1 take part; others are not looked at,
+ * whatever they hold.  No row at all gives out = 0 and lse = -inf.  Every
+ * sum is in float32 in a fixed order: the same call gives the same bits.
+ * q, k_new, v_new and out must be 16-byte aligned (VSD_ERR_ARG).
+ * Needs n <= max_tokens_per_req (else VSD_DEV_BAD_SEQLEN) and the pages of
+ * the rows that it reads or writes inside the pool (else VSD_DEV_BAD_PAGE): a
+ * rejected request, like an idle slot, gets out = 0 and lse = -inf, and
+ * neither the cache nor its scores change. */
+vsd_status vsd_decode_attention(const vsd_model* m, vsd_kv* kv, int32_t layer, int32_t batch,
+                                const int32_t* seq_lens_dev, const uint16_t* q_dev,
+                                const uint16_t* k_new_dev, const uint16_t* v_new_dev, int32_t window,
+                                float* score_dev, uint16_t* out_dev, float* lse_dev, vsd_stream stream);
+
+/* Cuts requests 0..B-1 to at most `budget` rows, by accumulated attention
+ * weight.  A request with L > budget rows keeps, in each layer and KV head on
+ * its own, its first `sinks` rows, its last `recent` rows and, of those
+ * between, the budget - sinks - recent with the largest score (among equal
+ * scores the lowest rows; NaN below every number).  Kept rows keep their
+ * order and move to rows 0..budget-1 of the same pages, K, V and score alike;
+ * nothing behind row budget-1 changes.
+ *   seq_lens_dev int32 [B] in: L_b
+ *   new_lens_dev int32 [B] out: min(L_b, budget); may be seq_lens_dev itself,
+ *                else must not overlap it
+ *   score_dev float32 [layers, B, n_kv, max_tokens_per_req] in/out: one
+ *             vsd_decode_attention score array per layer; NULL only when
+ *             sinks + recent = budget
+ *   kept_dev  optional int32 [layers, B, n_kv, budget] out: the former row of
+ *             each kept row, -1 behind the last
+ * A row keeps the position that its K was rotated for, but the step derives
+ * positions from lengths: a request that was cut goes on with
+ * vsd_decode_attention (whose caller rotates q and K), not with
+ * vsd_verify_step.
+ * L_b outside [0, max_tokens_per_req] (VSD_DEV_BAD_SEQLEN; -1, an idle slot,
+ * is no error) or a page of rows [0, L_b) outside the pool
+ * (VSD_DEV_BAD_PAGE) leaves the request as it was: new_lens = L_b, kept -1. */
+vsd_status vsd_kv_evict(vsd_kv* kv, int32_t batch, const int32_t* seq_lens_dev, int32_t* new_lens_dev,
+                        float* score_dev, int32_t budget, int32_t sinks, int32_t recent, int32_t* kept_dev,
+                        vsd_stream stream);
+
+/* One token from each row of logits, with the caller's uniforms.  With
+ * w_v = exp((x_v - max x) / T) and the ids in the order of falling logits
+ * (equal logits: lowest id first), the tokens kept are, in turn,
+ *   top_k: the first k;
+ *   top_p: of those the shortest prefix whose mass is >= p times theirs (at
+ *          least one);
+ *   min_p: of those the ones with w >= min_p (at least one);
+ * and the token is the smallest id whose cumulative kept mass reaches u times
+ * the kept total (the inverse CDF over ids of vsd_verify_step_sampled).
+ *   logits_dev float32 [rows] rows of `vocab` values, ld floats apart; NaN and
+ *              -inf are never sampled
+ *   temperature_dev float32 [rows] or NULL (1); T <= 0 or NaN: the largest
+ *              logit, lowest id first, whatever the filters
+ *   top_k_dev  int32 [rows] or NULL; k <= 0 or >= vocab: off
+ *   top_p_dev  float32 [rows] or NULL; p >= 1 or NaN: off
+ *   min_p_dev  float32 [rows] or NULL; <= 0 or NaN: off; above 1 counts as 1
+ *   u_dev      float32 [rows], in (0, 1); values outside are clamped to it
+ *   tokens_dev int32 [rows] out: -1 for a row with nothing to sample
+ *   logprob_dev optional float32 [rows] out: log of the token's share of the
+ *              kept mass (0 for T <= 0, -inf for a row with nothing)
+ * Weights are rounded to 2^-44 of the largest and summed as integers, so that
+ * a token does not depend on any order of summation.  rows = 0 does nothing;
+ * vocab <= 2^18 (VSD_ERR_UNSUPPORTED above). */
+vsd_status vsd_sample_logits(const float* logits_dev, int32_t rows, int32_t vocab, int64_t ld,
+                             const float* temperature_dev, const int32_t* top_k_dev,
+                             const float* top_p_dev, const float* min_p_dev, const float* u_dev,
+                             int32_t* tokens_dev, float* logprob_dev, vsd_stream stream);
+
 /* ---------------------------------------------------------------- components
  * Single kernels of the step, exposed so that each can be checked alone.  */
 

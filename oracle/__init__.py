@@ -15,5 +15,6 @@ Modules:
   weights  -- canonical (quantised) weight entries from BF16 master weights
   loop     -- slot scheduling of the device-resident draft / verify loop
   sampling -- stochastic (temperature) block verification, random numbers as inputs
+  serving  -- single-token decode attention, cache eviction, filtered sampling
 """
-from . import formats, quant, model, weights, loop, sampling  # noqa: F401
+from . import formats, quant, model, weights, loop, sampling, serving  # noqa: F401

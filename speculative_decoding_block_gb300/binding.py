@@ -31,6 +31,7 @@ EXPORTS = [
     "vsd_trace_enable", "vsd_trace_read", "vsd_debug_wait_probe", "vsd_kv_set_step_kernel",
     "vsd_ssm_create", "vsd_ssm_destroy", "vsd_ssm_set_state", "vsd_ssm_get_state", "vsd_ssm_verify",
     "vsd_ssm_commit", "vsd_ssm_get_device_status",
+    "vsd_kv_pools", "vsd_decode_attention", "vsd_kv_evict", "vsd_sample_logits",
 ]
 KERNEL_KINDS = ["embed", "qkv_gemm", "attention", "o_proj_gemm", "gate_up_gemm", "down_gemm",
                 "lm_head_gemm", "accept_commit", "step"]
@@ -112,6 +113,10 @@ def lib() -> ctypes.CDLL:
             "vsd_trace_read": ([p, p, c_int, ctypes.POINTER(c_int), p], c_int),
             "vsd_block_attention": ([p, p, c_int, c_int, p, p, p, p, p, p], c_int),
             "vsd_block_attention_static": ([p, p, c_int, c_int, p, p, p, p, p, p], c_int),
+            "vsd_kv_pools": ([p, ctypes.POINTER(p), ctypes.POINTER(p)], c_int),
+            "vsd_decode_attention": ([p, p, c_int, c_int, p, p, p, p, c_int, p, p, p, p], c_int),
+            "vsd_kv_evict": ([p, c_int, p, p, p, c_int, c_int, c_int, p, p], c_int),
+            "vsd_sample_logits": ([p, c_int, c_int, ctypes.c_int64, p, p, p, p, p, p, p, p], c_int),
             "vsd_accept_commit": ([p, p, c_int, p, p, p, p, p, p, p, p, p], c_int),
         }
         for name, (args, res) in sig.items():
@@ -478,3 +483,68 @@ def vsd_accept_commit(model: Model, kv: KV, batch: int, logits, k_new, v_new, se
                                    _dev(seq_lens, I32, "seq_lens", batch), _dev(pending, I32, "pending", batch),
                                    _dev(drafts, I32, "drafts", batch * 16), _dev(accepted, I32, "accepted", batch),
                                    _dev(out_tokens, I32, "out_tokens", batch * 17), _stream(stream)))
+
+
+class _Pool:
+    """Device memory of a cache's pool, as torch.as_tensor reads it; keeps the cache alive."""
+
+    def __init__(self, kv: KV, ptr: int, shape: tuple):
+        self.kv = kv
+        self.__cuda_array_interface__ = {"shape": shape, "typestr": "<i2", "data": (ptr, False), "version": 3}
+
+
+def vsd_kv_pools(kv: KV):
+    """The cache's K and V pools as BF16 tensors [layers, num_pages, n_kv, 16, head_dim] over its own memory."""
+    k, v = ctypes.c_void_p(), ctypes.c_void_p()
+    _check(lib().vsd_kv_pools(kv.handle, ctypes.byref(k), ctypes.byref(v)))
+    c = kv.model.cfg
+    shape = (c.layers, kv.num_pages, c.n_kv, 16, c.head_dim)
+    return tuple(torch.as_tensor(_Pool(kv, x.value, shape), device="cuda").view(torch.bfloat16) for x in (k, v))
+
+
+def vsd_decode_attention(model: Model, kv: KV, layer: int, batch: int, seq_lens, q, k_new, v_new, out, window: int = 0,
+                         score=None, lse=None, stream=None) -> None:
+    """One new token per request over the paged cache; k_new and v_new (or None for both) join it at row seq_lens[b].
+
+    score: float32 [batch, n_kv, max_tokens], to which the attention weights are added."""
+    c = model.cfg
+    n_q, n_kv = batch * c.n_q * c.head_dim, batch * c.n_kv * c.head_dim
+    _check(lib().vsd_decode_attention(model.handle, kv.handle, layer, batch, _dev(seq_lens, I32, "seq_lens", batch),
+                                      _dev(q, B16, "q", n_q), _dev(k_new, B16, "k_new", n_kv),
+                                      _dev(v_new, B16, "v_new", n_kv), int(window),
+                                      _dev(score, F32, "score", batch * c.n_kv * kv.max_tokens),
+                                      _dev(out, (torch.float16,), "out", n_q), _dev(lse, F32, "lse", batch * c.n_q),
+                                      _stream(stream)))
+
+
+def vsd_kv_evict(kv: KV, batch: int, seq_lens, new_lens, score, budget: int, sinks: int = 0, recent: int = 0, kept=None,
+                 stream=None) -> None:
+    """Cuts the requests to at most `budget` rows by accumulated attention weight, in place.
+
+    score: float32 [layers, batch, n_kv, max_tokens]; kept: optional int32 [layers, batch, n_kv, budget]."""
+    c = kv.model.cfg
+    heads = c.layers * batch * c.n_kv
+    _check(lib().vsd_kv_evict(kv.handle, batch, _dev(seq_lens, I32, "seq_lens", batch),
+                              _dev(new_lens, I32, "new_lens", batch), _dev(score, F32, "score", heads * kv.max_tokens),
+                              int(budget), int(sinks), int(recent), _dev(kept, I32, "kept", heads * max(budget, 0)),
+                              _stream(stream)))
+
+
+def vsd_sample_logits(logits, u, tokens, temperature=None, top_k=None, top_p=None, min_p=None, logprob=None,
+                      stream=None) -> None:
+    """One token per row of logits (float32 [rows, vocab], rows any distance apart)."""
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+        raise TypeError("logits must be a CUDA tensor")
+    if logits.dtype != torch.float32:
+        raise TypeError(f"logits has dtype {logits.dtype}, expected float32")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [rows, vocab] with adjacent values in a row")
+    rows, vocab = logits.shape
+    ld = logits.stride(0) if rows > 1 else vocab
+    if ld < vocab:
+        raise ValueError("logits has overlapping rows")
+    _check(lib().vsd_sample_logits(ctypes.c_void_p(logits.data_ptr()), rows, vocab, ld,
+                                   _dev(temperature, F32, "temperature", rows), _dev(top_k, I32, "top_k", rows),
+                                   _dev(top_p, F32, "top_p", rows), _dev(min_p, F32, "min_p", rows),
+                                   _dev(u, F32, "u", rows), _dev(tokens, I32, "tokens", rows),
+                                   _dev(logprob, F32, "logprob", rows), _stream(stream)))

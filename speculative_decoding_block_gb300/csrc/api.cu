@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "host_util.h"
+#include "kv_view.h"
 #include "launch.h"
 #include "quant_kernels.cuh"
 #include "step_kernels.cuh"
@@ -163,6 +164,12 @@ struct vsd_kv {
   CUtensorMap tm_u[kActBoxes]{}, tm_o[kActBoxes]{}, tm_a[kActBoxes]{};
   CUtensorMap tm_q{}, tm_kc{}, tm_vc{}, tm_kn{}, tm_vn{};
 };
+
+vsd::KvView vsd::kv_view(const vsd_kv* kv) {
+  const vsd_model_config& c = kv->m->cfg;
+  return {kv->m,       c.layers,  c.n_q,      c.n_kv,     c.head_dim,     kv->max_batch, kv->max_tokens, kv->num_pages,
+          kv->ppr,     kv->m->sms, kv->k_pool, kv->v_pool, kv->page_table, kv->status,    kv->tm_kc,      kv->tm_vc};
+}
 
 namespace {
 

@@ -1,0 +1,144 @@
+// serve.cu -- host side of the single-token serving operators: decode
+// attention over the paged cache, eviction by accumulated attention weight,
+// and token sampling.
+#include <cmath>
+#include <cstdint>
+
+#include "decode_attention.cuh"
+#include "evict.cuh"
+#include "host_util.h"
+#include "kv_view.h"
+#include "sample.cuh"
+
+using namespace vsd;
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+}  // namespace
+
+extern "C" {
+
+vsd_status vsd_kv_pools(const vsd_kv* kv, uint16_t** k, uint16_t** v) {
+  if (!kv || !k || !v) return fail(VSD_ERR_ARG, "NULL pointer");
+  const KvView c = kv_view(kv);
+  *k = reinterpret_cast<uint16_t*>(c.k_pool);
+  *v = reinterpret_cast<uint16_t*>(c.v_pool);
+  return VSD_OK;
+}
+
+vsd_status vsd_decode_attention(const vsd_model* m, vsd_kv* kv, int32_t layer, int32_t batch, const int32_t* seq_lens,
+                                const uint16_t* q, const uint16_t* k_new, const uint16_t* v_new, int32_t window,
+                                float* score, uint16_t* out, float* lse, vsd_stream stream) {
+  if (!m || !kv || !seq_lens || !q || !out) return fail(VSD_ERR_ARG, "NULL pointer");
+  if (!k_new != !v_new) return fail(VSD_ERR_ARG, "k_new and v_new go together");
+  const KvView c = kv_view(kv);
+  if (c.model != m) return fail(VSD_ERR_ARG, "the cache was created for another model");
+  if (batch < 1 || batch > c.max_batch || layer < 0 || layer >= c.layers)
+    return fail(VSD_ERR_ARG, "batch or layer out of range");
+  if (window < 0) return fail(VSD_ERR_ARG, "window %d below 0", window);
+  if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(out))
+    return fail(VSD_ERR_ARG, "q, k_new, v_new and out must be 16-byte aligned");
+  DecodeArgs a{};
+  a.batch = batch;
+  a.n_q = c.n_q;
+  a.n_kv = c.n_kv;
+  a.group = c.n_q / c.n_kv;
+  a.layer = layer;
+  a.num_pages = c.num_pages;
+  a.ppr = c.ppr;
+  a.max_tokens = c.max_tokens;
+  a.window = window;
+  a.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(c.hd)));
+  a.lens = seq_lens;
+  a.page_table = c.page_table;
+  a.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  a.k_new = reinterpret_cast<const __nv_bfloat16*>(k_new);
+  a.v_new = reinterpret_cast<const __nv_bfloat16*>(v_new);
+  a.k_pool = c.k_pool;
+  a.v_pool = c.v_pool;
+  a.out = reinterpret_cast<__half*>(out);
+  a.lse = lse;
+  a.score = score;
+  a.status = c.status;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int grid = batch * c.n_kv;
+  if (c.hd == 64) decode_attention_kernel<64><<<grid, kDecodeThreads, 0, st>>>(a);
+  else decode_attention_kernel<128><<<grid, kDecodeThreads, 0, st>>>(a);
+  CK(cudaGetLastError());
+  return VSD_OK;
+}
+
+vsd_status vsd_kv_evict(vsd_kv* kv, int32_t batch, const int32_t* seq_lens, int32_t* new_lens, float* score,
+                        int32_t budget, int32_t sinks, int32_t recent, int32_t* kept, vsd_stream stream) {
+  if (!kv || !seq_lens || !new_lens) return fail(VSD_ERR_ARG, "NULL pointer");
+  const KvView c = kv_view(kv);
+  if (batch < 1 || batch > c.max_batch) return fail(VSD_ERR_ARG, "batch %d outside [1, %d]", batch, c.max_batch);
+  if (budget < 1 || sinks < 0 || recent < 0 || static_cast<int64_t>(sinks) + recent > budget)
+    return fail(VSD_ERR_ARG, "need budget >= 1, sinks >= 0, recent >= 0 and sinks + recent <= budget");
+  if (!score && static_cast<int64_t>(sinks) + recent < budget)
+    return fail(VSD_ERR_ARG, "score is NULL and sinks + recent leave rows to choose");
+  const size_t nb = static_cast<size_t>(batch) * sizeof(int32_t);
+  if (new_lens != seq_lens && overlap(new_lens, nb, seq_lens, nb))
+    return fail(VSD_ERR_ARG, "new_lens must be seq_lens itself or apart from it");
+  EvictArgs a{};
+  a.batch = batch;
+  a.layers = c.layers;
+  a.n_kv = c.n_kv;
+  a.num_pages = c.num_pages;
+  a.ppr = c.ppr;
+  a.max_tokens = c.max_tokens;
+  a.budget = budget;
+  a.sinks = sinks;
+  a.recent = recent;
+  a.lens = seq_lens;
+  a.new_lens = new_lens == seq_lens ? nullptr : new_lens;
+  a.page_table = c.page_table;
+  a.k_pool = c.k_pool;
+  a.v_pool = c.v_pool;
+  a.score = score;
+  a.kept = kept;
+  a.status = c.status;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int grid = c.layers * batch * c.n_kv;
+  if (c.hd == 64) evict_kernel<64><<<grid, kEvictThreads, 0, st>>>(a);
+  else evict_kernel<128><<<grid, kEvictThreads, 0, st>>>(a);
+  CK(cudaGetLastError());
+  if (!a.new_lens) {
+    evict_lens_kernel<<<batch, kEvictThreads, 0, st>>>(a, new_lens);
+    CK(cudaGetLastError());
+  }
+  return VSD_OK;
+}
+
+vsd_status vsd_sample_logits(const float* logits, int32_t rows, int32_t vocab, int64_t ld, const float* temperature,
+                             const int32_t* top_k, const float* top_p, const float* min_p, const float* u,
+                             int32_t* tokens, float* logprob, vsd_stream stream) {
+  if (rows < 0 || vocab < 1 || ld < vocab) return fail(VSD_ERR_ARG, "need rows >= 0, vocab >= 1 and ld >= vocab");
+  if (vocab > kMaxSampleVocab) return fail(VSD_ERR_UNSUPPORTED, "vocab %d above %d", vocab, kMaxSampleVocab);
+  if (rows == 0) return VSD_OK;
+  if (!logits || !u || !tokens) return fail(VSD_ERR_ARG, "NULL pointer");
+  SampleRowArgs a{};
+  a.logits = logits;
+  a.ld = ld;
+  a.rows = rows;
+  a.vocab = vocab;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.u = u;
+  a.tokens = tokens;
+  a.logprob = logprob;
+  sample_logits_kernel<<<rows, kSampleThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  CK(cudaGetLastError());
+  return VSD_OK;
+}
+
+}  // extern "C"
