@@ -453,10 +453,11 @@ vsd_status vsd_kv_get_anchor(const vsd_kv* kv, int32_t batch, float* dst_dev, vs
  * What a request needs next to block verification when one token at a time is
  * produced: attention of its new token over the same paged cache, a cache that
  * can be cut to a budget of rows, and a token drawn from a row of logits.
- * Asynchronous; no allocation, no workspace of the cache is used, so calls may
- * be captured in CUDA graphs, and calls on different streams may overlap as
- * long as they touch different requests' rows.  Pointers belong to the device
- * that is current, which must be the cache's. */
+ * Asynchronous, without allocation or host round trips, so calls may be
+ * captured in CUDA graphs.  The attention runs in the cache's workspace: two
+ * calls, or a call and a verify or draft step, of one cache must not overlap
+ * on the GPU (order them on one stream; different caches are independent).
+ * Pointers belong to the current device, which must be the cache's. */
 
 /* Device addresses of the cache's K and V pools, BF16
  * [layers][num_pages][n_kv][16][head_dim] (row i of request b: page-table

@@ -128,6 +128,8 @@ struct vsd_kv {
   float *attn_o = nullptr, *attn_ml = nullptr;
   int* attn_counters = nullptr;
   size_t attn_items_cap = 0;
+  float* decode_raw = nullptr;  // [max_batch][n_q][max_tokens] scores of the decode attention
+  int* decode_off = nullptr;    // [max_batch + 1] first piece of work of each request there
   float* anchor = nullptr;  // [max_batch][H] residual row of the last accepted position (drafter input)
   int* zeros = nullptr;     // [max_batch] zero context lengths (the draft pass reads no cache)
   int* probe_flag = nullptr;  // one int nothing ever sets (the wait probe's flag)
@@ -167,8 +169,28 @@ struct vsd_kv {
 
 vsd::KvView vsd::kv_view(const vsd_kv* kv) {
   const vsd_model_config& c = kv->m->cfg;
-  return {kv->m,       c.layers,  c.n_q,      c.n_kv,     c.head_dim,     kv->max_batch, kv->max_tokens, kv->num_pages,
-          kv->ppr,     kv->m->sms, kv->k_pool, kv->v_pool, kv->page_table, kv->status,    kv->tm_kc,      kv->tm_vc};
+  KvView v{};
+  v.model = kv->m;
+  v.layers = c.layers;
+  v.n_q = c.n_q;
+  v.n_kv = c.n_kv;
+  v.hd = c.head_dim;
+  v.max_batch = kv->max_batch;
+  v.max_tokens = kv->max_tokens;
+  v.num_pages = kv->num_pages;
+  v.ppr = kv->ppr;
+  v.sms = kv->m->sms;
+  v.k_pool = kv->k_pool;
+  v.v_pool = kv->v_pool;
+  v.page_table = kv->page_table;
+  v.status = kv->status;
+  v.ws_o = kv->attn_o;
+  v.ws_ml = kv->attn_ml;
+  v.ws_off = kv->decode_off;
+  v.ws_floats_o = kv->attn_items_cap * 128 * c.head_dim;
+  v.ws_floats_ml = kv->attn_items_cap * 128 * 2;
+  v.ws_raw = kv->decode_raw;
+  return v;
 }
 
 namespace {
@@ -706,7 +728,9 @@ vsd_status vsd_kv_create(const vsd_model* m, int32_t max_batch, int32_t max_toke
   kv->attn_items_cap = static_cast<size_t>(4) * m->sms + static_cast<size_t>(2) * max_batch * c.n_kv;
   if ((s = dalloc(&kv->attn_o, kv->attn_items_cap * 128 * hd, false)) ||
       (s = dalloc(&kv->attn_ml, kv->attn_items_cap * 128 * 2, false)) ||
-      (s = dalloc(&kv->attn_counters, static_cast<size_t>(2) * max_batch * c.n_kv)))
+      (s = dalloc(&kv->attn_counters, static_cast<size_t>(2) * max_batch * c.n_kv)) ||
+      (s = dalloc(&kv->decode_raw, static_cast<size_t>(max_batch) * c.n_q * max_tokens, false)) ||
+      (s = dalloc(&kv->decode_off, static_cast<size_t>(max_batch) + 1)))
     return cleanup(s);
   const auto F16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16, BF16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   for (int j = 0; j < kActBoxes; ++j) {
@@ -735,7 +759,7 @@ void vsd_kv_destroy(vsd_kv* kv) {
   if (kv->io_host) cudaFreeHost(kv->io_host);
   void* ptrs[] = {kv->k_pool, kv->v_pool, kv->page_table, kv->x, kv->u, kv->act_o, kv->act_a, kv->q_tile,
                   kv->k_new, kv->v_new, kv->keys, kv->ctx_len, kv->req_ok, kv->ssq, kv->attn_o,
-                  kv->attn_ml, kv->attn_counters, kv->anchor, kv->zeros, kv->probe_flag, kv->loop_seq, kv->loop_pend,
+                  kv->attn_ml, kv->attn_counters, kv->decode_raw, kv->decode_off, kv->anchor, kv->zeros, kv->probe_flag, kv->loop_seq, kv->loop_pend,
                   kv->loop_drafts, kv->loop_acc, kv->loop_out, kv->tile_max, kv->tile_sum, kv->draft_logit, kv->decided,
                   kv->status, kv->trace, kv->mk_sync, kv->mk_part, kv->mk_item_cnt};
   for (void* p : ptrs)

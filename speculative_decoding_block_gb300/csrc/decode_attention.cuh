@@ -7,6 +7,27 @@
 //     s_i = q . K_i / sqrt(hd),  p = softmax(s),  o = sum_i p_i V_i,
 // with the running maximum and sum of the online softmax, so that K and V
 // are read once.  Rows outside the set never take part, whatever they hold.
+//
+// Bound by the K and V bytes (two flops a byte and query head), so the first
+// kernel is laid out for bytes in flight and for even shares: the rows of
+// every (request, KV head) pair are cut into stages of 8 KB of K and V, and
+// all stages of the call, in order, are dealt in equal contiguous ranges to
+// the warps of one CTA per SM, whatever the lengths.  A warp's range covers
+// parts of one or more pairs ("segments"); it owns a ring of stages filled by
+// cp.async through the page table and waits for no other warp.  Per stage:
+// S = Q K^T and O += P V as mma.sync tiles of 16 x 8 -- a tcgen05 tile has 128
+// rows, a group up to 7 -- with the sixteen rows of the second product holding
+// each head's weights twice, as bf16(p) and bf16(p - bf16(p)), whose sums meet
+// in one thread's accumulators (p keeps 16 bits).  Each segment leaves a
+// record (maximum, sum, unnormalised output) in the cache's workspace.
+//
+// The second kernel joins a pair's records in their order and does what needs
+// the joined maximum and sum: the outputs, the new row's place in the cache,
+// the accumulated weights (from the scores that the first kernel left in the
+// workspace, 4 bytes a row and query head, mostly met again in L2).  A join
+// inside one cooperative launch, by waiting CTAs, took 12-18 us of the 25-38
+// of 32 requests of 1024-8192 rows, most of it in once-run code and waits;
+// two launches need no wait at all.
 #pragma once
 
 #include "vsd_common.cuh"
@@ -17,6 +38,8 @@ constexpr int kMaxGroup = 7;  // query heads per KV head (a model's 17-row verif
 
 struct DecodeArgs {
   int batch, n_q, n_kv, group, layer, num_pages, ppr, max_tokens, window;
+  int warps;                // of the first kernel's grid
+  int chunks;               // CTAs per pair of the second kernel
   float scale_log2;         // log2(e) / sqrt(hd)
   const int* lens;          // [B] cached rows (-1: idle slot)
   const int* page_table;    // [max_batch][ppr]
@@ -27,140 +50,505 @@ struct DecodeArgs {
   __half* out;   // [B][n_q][hd]
   float* lse;    // [B][n_q] or nullptr
   float* score;  // [B][n_kv][max_tokens] or nullptr
+  // workspace: a record per segment (number: its warp's + its pair's)
+  int* off;      // [B + 1] first stage of each request, over all its KV heads
+  float* rec_o;  // [record][group][hd] unnormalised output
+  float* rec_ml; // [record][16]: maxima (raw scores) of 8 heads, sums of 7, the flag of a page outside the pool
+  float* raw;    // [B][n_q][max_tokens] scores of the rows, when `score` is given
   int* status;
 };
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
+constexpr int kDecWarps = 8;
+constexpr int kDecThreads = 32 * kDecWarps;
+constexpr int kDecStages = 2;  // 128 KB of rings per CTA; 3 stages, 4 stages of 6 warps or 2 of 12 measured the same within 3 %
+constexpr int kDecStageBytes = 8192;  // K rows, then V rows
+constexpr int kDecMaxReqs = 1024;
+constexpr int kJoinThreads = 256;
+__host__ __device__ constexpr int dec_stage_rows(int hd) { return kDecStageBytes / (4 * hd); }
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// D += A B, 16 x 8 x 16, bf16 in, f32 out.
+__device__ __forceinline__ void mma_bf16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void cp_async16_hint(uint32_t dst, const void* src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Scale of values taken against maximum m when the joined one is `base` (log2 units).
+__device__ __forceinline__ float rescale(float m, float sl, float base) { return ex2(m * sl - base); }
+__device__ __forceinline__ float log2_base(float m, float sl) { return m == -INFINITY ? 0.0f : m * sl; }
+
+// What a request attends to.
+struct DecodeReq {
+  int L, n, lo, st_lo, stages;  // cached rows, rows in all (0: nothing to do), first row, first stage, stages
+  bool valid;
+};
+template <int HD>
+__device__ __forceinline__ DecodeReq decode_request(const DecodeArgs& a, int b) {
+  constexpr int SR = dec_stage_rows(HD);
+  const int more = a.k_new != nullptr ? 1 : 0;
+  DecodeReq r;
+  r.L = a.lens[b];
+  r.valid = r.L >= 0 && r.L + more <= a.max_tokens;
+  r.n = r.valid ? r.L + more : 0;
+  r.lo = a.window > 0 ? min(max(r.L, 0), max(0, r.n - a.window)) : 0;
+  r.st_lo = r.lo / SR;
+  r.stages = r.n > 0 && r.L > r.lo ? (r.L + SR - 1) / SR - r.st_lo : 0;
+  return r;
 }
 
-// One CTA per (request, KV head); its eight warps walk the rows in turn,
-// each with its own running maximum, sum and output per query head, joined
-// through shared memory at the end.
-constexpr int kDecodeThreads = 256;
+// How the T stages of a call are dealt: the first `extra` warps take one more than the others.
+struct DecodeShares {
+  int warps, each, extra;  // warps with work
+  __device__ __forceinline__ DecodeShares(int total, int grid_warps) {
+    warps = max(1, min(grid_warps, total));
+    each = total / warps;
+    extra = total - each * warps;
+  }
+  __device__ __forceinline__ int first(int w) const { return w * each + min(w, extra); }
+  __device__ __forceinline__ int warp_of(int it) const {
+    const int big = extra * (each + 1);
+    return it < big ? it / (each + 1) : extra + (it - big) / each;
+  }
+};
+
+// Score of the new row for this lane's query head (lane = 4 * head + quad; the quad's four lanes share it).
+template <int HD>
+__device__ __forceinline__ float new_row_score(const DecodeArgs& a, int b, int h, int head, int quad) {
+  constexpr int C = HD / 32;  // 16-byte chunks per lane
+  float d = 0.0f;
+  if (head < a.group) {
+    const uint4* x = reinterpret_cast<const uint4*>(a.q + (static_cast<size_t>(b) * a.n_q + h * a.group + head) * HD) + quad * C;
+    const uint4* y = reinterpret_cast<const uint4*>(a.k_new + (static_cast<size_t>(b) * a.n_kv + h) * HD) + quad * C;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const uint4 u = x[c], v = y[c];
+      const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        d += __uint_as_float(uw[e] << 16) * __uint_as_float(vw[e] << 16) +
+             __uint_as_float(uw[e] & 0xFFFF0000u) * __uint_as_float(vw[e] & 0xFFFF0000u);
+    }
+  }
+  d += __shfl_xor_sync(0xFFFFFFFFu, d, 1);
+  return d + __shfl_xor_sync(0xFFFFFFFFu, d, 2);
+}
 
 template <int HD>
-__global__ void __launch_bounds__(kDecodeThreads) decode_attention_kernel(const DecodeArgs a) {
-  constexpr int E = HD / 32;  // elements of a row per lane
-  constexpr int W = kDecodeThreads / 32;
-  __shared__ float m_s[W][kMaxGroup], l_s[W][kMaxGroup], o_s[W][kMaxGroup][HD];
-  __shared__ int bad_s;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.x / a.n_kv, h = blockIdx.x % a.n_kv, g = a.group;
-  const int L = a.lens[b];
+__global__ void __launch_bounds__(kDecThreads, 1) decode_stream_kernel(const DecodeArgs a) {
+  constexpr int SR = dec_stage_rows(HD);  // rows of a stage
+  constexpr int PS = SR / kPage;          // pages of a stage
+  constexpr int NA = HD / 64;             // 128-byte column blocks of a row
+  constexpr int NT = SR / 8;              // 8-row tiles of S
+  constexpr int KS = HD / 16;             // 16-wide steps of S's product
+  constexpr int RC = HD / 8;              // 16-byte chunks of a row
+  constexpr uint32_t BOX = kPage * 128;   // bytes of a block of 16 rows of 128, 128-byte swizzled
+  constexpr uint32_t VOFF = kDecStageBytes / 2;
+  extern __shared__ __align__(1024) uint8_t smem[];  // the rings
+  __shared__ int off[kDecMaxReqs + 1];
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, head = lane >> 2, quad = lane & 3;
+  const int g = a.group;
   const bool append = a.k_new != nullptr;
-  if (threadIdx.x == 0) bad_s = 0;
-  __syncthreads();
-  const bool valid = L >= 0 && L + (append ? 1 : 0) <= a.max_tokens;
-  if (!valid && L != kIdleSlot && threadIdx.x == 0) atomicOr(a.status, VSD_DEV_BAD_SEQLEN);
-  const int n = valid ? L + (append ? 1 : 0) : 0;
-  const int lo = a.window > 0 ? max(0, n - a.window) : 0;
-  const int* pages = a.page_table + static_cast<size_t>(b) * a.ppr;
-  auto row_offset = [&](int i) -> size_t {
-    int page = pages[i / kPage];
-    if (page < 0 || page >= a.num_pages) {
-      bad_s = 1;
-      page = 0;
+  const float sl = a.scale_log2;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (warp == 0) {
+    int base = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      const int b = b0 + lane, cnt = b < a.batch ? decode_request<HD>(a, b).stages * a.n_kv : 0;
+      int incl = cnt;
+#pragma unroll
+      for (int w = 1; w < 32; w <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, incl, w);
+        if (lane >= w) incl += y;
+      }
+      if (b < a.batch) {
+        off[b] = base + incl - cnt;
+        if (blockIdx.x == 0) a.off[b] = base + incl - cnt;
+      }
+      base += __shfl_sync(0xFFFFFFFFu, incl, 31);
     }
-    return (((static_cast<size_t>(a.layer) * a.num_pages + page) * a.n_kv + h) * kPage + i % kPage) * HD;
-  };
-  float q[kMaxGroup][E], o[kMaxGroup][E], m[kMaxGroup], l[kMaxGroup];
-#pragma unroll
-  for (int j = 0; j < kMaxGroup; ++j) {
-    m[j] = -INFINITY;
-    l[j] = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      o[j][e] = 0.0f;
-      q[j][e] = j < g ? __bfloat162float(a.q[(static_cast<size_t>(b) * a.n_q + h * g + j) * HD + lane * E + e]) : 0.0f;
-    }
-  }
-  const size_t new_off = (static_cast<size_t>(b) * a.n_kv + h) * HD;
-  // scores of row i for every query head of the group, in log2 units
-  auto scores = [&](int i, float* s) {
-    const __nv_bfloat16* k = (append && i == L) ? a.k_new + new_off : a.k_pool + row_offset(i);
-    float kf[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) kf[e] = __bfloat162float(k[lane * E + e]);
-#pragma unroll
-    for (int j = 0; j < kMaxGroup; ++j) {
-      float d = 0.0f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) d += q[j][e] * kf[e];
-      s[j] = warp_sum(d) * a.scale_log2;
-    }
-  };
-  for (int i = lo + warp; i < n; i += W) {
-    float s[kMaxGroup];
-    scores(i, s);
-    const __nv_bfloat16* v = (append && i == L) ? a.v_new + new_off : a.v_pool + row_offset(i);
-    float vf[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) vf[e] = __bfloat162float(v[lane * E + e]);
-#pragma unroll
-    for (int j = 0; j < kMaxGroup; ++j) {
-      const float mn = fmaxf(m[j], s[j]), mu = mn == -INFINITY ? 0.0f : mn;
-      const float c = exp2f(m[j] - mu), p = exp2f(s[j] - mu);
-      m[j] = mn;
-      l[j] = l[j] * c + p;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[j][e] = o[j][e] * c + p * vf[e];
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < kMaxGroup; ++j) {
     if (lane == 0) {
-      m_s[warp][j] = m[j];
-      l_s[warp][j] = l[j];
+      off[a.batch] = base;
+      if (blockIdx.x == 0) a.off[a.batch] = base;
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) o_s[warp][j][lane * E + e] = o[j][e];
   }
-  // the new row's page is checked before anything is written
-  if (append && valid && threadIdx.x == 0) row_offset(L);
   __syncthreads();
-  const bool bad = bad_s != 0;
-  if (bad && threadIdx.x == 0) atomicOr(a.status, VSD_DEV_BAD_PAGE);
-  const bool empty = bad || n == 0;
-  auto join = [&](int j, float& mj, float& lj) {
-    mj = -INFINITY;
-    for (int w = 0; w < W; ++w) mj = fmaxf(mj, m_s[w][j]);
-    if (mj == -INFINITY) mj = 0.0f;
-    lj = 0.0f;
-    for (int w = 0; w < W; ++w) lj += l_s[w][j] * exp2f(m_s[w][j] - mj);
-  };
-  for (int i = threadIdx.x; i < g * HD; i += kDecodeThreads) {
-    const int j = i / HD, d = i % HD;
-    float mj, lj, acc = 0.0f;
-    join(j, mj, lj);
-    for (int w = 0; w < W; ++w) acc += o_s[w][j][d] * exp2f(m_s[w][j] - mj);
-    // one rounding, to the GEMM input type
-    a.out[(static_cast<size_t>(b) * a.n_q + h * g) * HD + i] = __float2half_rn(empty ? 0.0f : acc / lj);
-    if (d == 0 && a.lse)
-      a.lse[static_cast<size_t>(b) * a.n_q + h * g + j] = empty ? -INFINITY : (mj + log2f(lj)) * 0.69314718f;
+  // this warp's stages; warps are numbered across the CTAs, so that a short call spreads over the SMs
+  const int gw = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+  const DecodeShares share(off[a.batch], a.warps);
+  if (gw >= share.warps || off[a.batch] == 0) return;
+  const int it0 = share.first(gw), it1 = share.first(gw + 1);
+  const uint32_t ring_u = smem_u32(smem + warp * kDecStages * kDecStageBytes);
+  const uint64_t pol = policy_evict_first();
+
+#pragma unroll 1
+  for (int it = it0; it < it1;) {
+    // the segment: stages [st, st + n_st) of pair (b, h)
+    int b = 0;
+    {
+      int hi = a.batch - 1;  // the last request that starts at or before `it` (one without stages starts with the next)
+#pragma unroll 1
+      while (b < hi) {
+        const int mid = (b + hi + 1) >> 1;
+        if (off[mid] <= it) b = mid;
+        else hi = mid - 1;
+      }
+    }
+    const DecodeReq r = decode_request<HD>(a, b);
+    const int rem = it - off[b], h = rem / r.stages, st = rem - h * r.stages, n_st = min(r.stages - st, it1 - it);
+    const int row0 = (r.st_lo + st) * SR;
+    const size_t hq = static_cast<size_t>(b) * a.n_q + h * g + (head < g ? head : 0);
+    it += n_st;
+    float o[HD / 8][4], m = -INFINITY, l = 0.0f;
+    int bad = 0;  // a page outside the pool
+#pragma unroll
+    for (int d = 0; d < HD / 8; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[d][e] = 0.0f;
+    // page-table entries 32 at a time, the next 32 read ahead
+    const int* pages = a.page_table + static_cast<size_t>(b) * a.ppr;
+    const int pg0 = (r.st_lo + st) * PS, page_lo = r.lo / kPage, page_hi = (r.L - 1) / kPage;
+    auto page_block = [&](int blk) { return pages[min(max(pg0 + blk * 32 + lane, page_lo), page_hi)]; };
+    int pg_cur = page_block(0), pg_next = n_st * PS > 32 ? page_block(1) : 0;
+    const size_t layer_head = (static_cast<size_t>(a.layer) * a.num_pages * a.n_kv + h) * kPage * HD + lane * 8;
+    uint32_t qa[KS][2];  // query fragments (rows 8..15 of the tile are zero)
+    // stage i is computed after stage i + kDecStages - 1 has been asked for
+#pragma unroll 1
+    for (int i = -kDecStages; i < n_st; ++i) {
+      if (i >= 0) {
+        cp_async_wait_group<kDecStages - 1>();
+        __syncwarp();
+        const uint32_t kb = ring_u + (i % kDecStages) * kDecStageBytes, vb = kb + VOFF;
+        const int first = row0 + i * SR;
+        // S: s[j][e] = score of row j * 8 + quad * 2 + e for this lane's head, -inf outside the set
+        float s[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int k = 0; k < KS; k += 2) {
+            uint32_t f[4];
+            ldsm_x4(kb + ((j / 2) * NA + k / 4) * BOX + sw128_off((j & 1) * 8 + (lane & 7), (k * 2 & 7) + (lane >> 3)), f);
+            mma_bf16(acc, qa[k][0], 0u, qa[k][1], 0u, f[0], f[1]);
+            mma_bf16(acc, qa[k + 1][0], 0u, qa[k + 1][1], 0u, f[2], f[3]);
+          }
+          s[j][0] = acc[0];
+          s[j][1] = acc[1];
+        }
+        if (first < r.lo || first + SR > r.L) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int row = first + j * 8 + quad * 2 + e;
+              if (row < r.lo || row >= r.L) s[j][e] = -INFINITY;
+            }
+          // V rows outside the set may hold anything, and 0 * NaN is NaN
+#pragma unroll 1
+          for (int y = lane; y < SR * RC; y += 32) {
+            const int row = y / RC, c = y % RC;
+            if (first + row < r.lo || first + row >= r.L)
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                               vb + ((row / kPage) * NA + c / 8) * BOX + sw128_off(row % kPage, c % 8)), "r"(0u)
+                           : "memory");
+          }
+          __syncwarp();
+        }
+        if (a.score && head < g) {
+          float* raw = a.raw + hq * a.max_tokens + first + quad * 2;
+          if (first + SR <= a.max_tokens && (a.max_tokens & 1) == 0) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) *reinterpret_cast<float2*>(raw + j * 8) = make_float2(s[j][0], s[j][1]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (first + j * 8 + quad * 2 + e < a.max_tokens) raw[j * 8 + e] = s[j][e];
+          }
+        }
+        float mx = m;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) mx = fmaxf(mx, fmaxf(s[j][0], s[j][1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+        const float base = log2_base(mx, sl);
+        if (__any_sync(0xFFFFFFFFu, mx > m)) {
+          const float c = rescale(m, sl, base);
+          l *= c;
+#pragma unroll
+          for (int d = 0; d < HD / 8; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[d][e] *= c;
+        }
+        m = mx;
+        uint32_t ph[NT], pl[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const float p0 = ex2(fmaf(s[j][0], sl, -base)), p1 = ex2(fmaf(s[j][1], sl, -base));
+          l += p0 + p1;
+          ph[j] = f32x2_to_bf16x2(p0, p1);
+          pl[j] = f32x2_to_bf16x2(p0 - __uint_as_float(ph[j] << 16), p1 - __uint_as_float(ph[j] & 0xFFFF0000u));
+        }
+#pragma unroll
+        for (int p = 0; p < PS; ++p) {
+#pragma unroll
+          for (int d = 0; d < HD / 8; d += 2) {
+            uint32_t v[4];
+            ldsm_x4_t(vb + (p * NA + d / 8) * BOX + sw128_off((lane & 7) + ((lane >> 3) & 1) * 8, (d & 7) + (lane >> 4)), v);
+            mma_bf16(o[d], ph[2 * p], pl[2 * p], ph[2 * p + 1], pl[2 * p + 1], v[0], v[1]);
+            mma_bf16(o[d + 1], ph[2 * p], pl[2 * p], ph[2 * p + 1], pl[2 * p + 1], v[2], v[3]);
+          }
+        }
+        __syncwarp();
+      }
+      const int ni = i + kDecStages;
+      if (ni < n_st) {
+        if (((ni * PS) & 31) == 0 && ni) {
+          pg_cur = pg_next;
+          if (ni * PS + 32 < n_st * PS) pg_next = page_block(((ni * PS) >> 5) + 1);
+        }
+        const uint32_t dst = ring_u + (ni % kDecStages) * kDecStageBytes;
+#pragma unroll
+        for (int p = 0; p < PS; ++p) {
+          int page = __shfl_sync(0xFFFFFFFFu, pg_cur, ((ni * PS) & 31) + p);
+          if (page < 0 || page >= a.num_pages) {
+            bad = 1;
+            page = 0;
+          }
+          const size_t src = layer_head + page * (static_cast<size_t>(a.n_kv) * kPage * HD);
+#pragma unroll
+          for (int u = 0; u < kPage * RC / 32; ++u) {
+            const int x16 = u * 32 + lane, row = x16 / RC, c = x16 % RC;
+            const uint32_t to = dst + (p * NA + c / 8) * BOX + sw128_off(row, c & 7);
+            cp_async16_hint(to, a.k_pool + src + u * 256, pol);
+            cp_async16_hint(to + VOFF, a.v_pool + src + u * 256, pol);
+          }
+        }
+      }
+      cp_async_commit();
+      if (i == -1) {  // what the products need is read while the first stages travel
+        const __nv_bfloat16* q = a.q + hq * HD;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const uint32_t* src = reinterpret_cast<const uint32_t*>(q + k * 16 + quad * 2);
+          qa[k][0] = head < g ? src[0] : 0u;
+          qa[k][1] = head < g ? src[4] : 0u;
+        }
+        if (append && st == 0) {
+          // the new row starts the pair's first segment: its weight is 1 against its own score
+          m = new_row_score<HD>(a, b, h, head, quad);
+          l = head < g && quad == 0 ? 1.0f : 0.0f;
+          const __nv_bfloat16* vn = a.v_new + (static_cast<size_t>(b) * a.n_kv + h) * HD;
+#pragma unroll
+          for (int d = 0; d < HD / 8; ++d) {
+            const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(vn + d * 8 + quad * 2));
+            o[d][0] = v.x;
+            o[d][1] = v.y;
+          }
+        }
+      }
+    }
+    l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
+    l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
+    const size_t rec = static_cast<size_t>(gw) + b * a.n_kv + h;
+    if (quad == 0) {
+      a.rec_ml[rec * 16 + head] = m;
+      a.rec_ml[rec * 16 + 8 + head] = head < 7 ? l : (bad ? 1.0f : 0.0f);
+    }
+    if (head < g) {
+      float* ro = a.rec_o + (rec * g + head) * HD + quad * 2;
+#pragma unroll
+      for (int d = 0; d < HD / 8; ++d)
+        *reinterpret_cast<float2*>(ro + d * 8) = make_float2(o[d][0] + o[d][2], o[d][1] + o[d][3]);
+    }
   }
-  if (empty) return;
-  if (a.score) {
-    float mj[kMaxGroup], lj[kMaxGroup];
-    for (int j = 0; j < g; ++j) join(j, mj[j], lj[j]);
-    float* score = a.score + (static_cast<size_t>(b) * a.n_kv + h) * a.max_tokens;
-    for (int i = lo + warp; i < n; i += W) {
-      float s[kMaxGroup];
-      scores(i, s);
-      float sum = 0.0f;
+}
+
+// `chunks` CTAs per pair: each joins the pair's maxima and sums, then its
+// share of the outputs and of the rows' weights.  A chain of dependent L2
+// round trips (lengths, shares, records, rows), so each step asks for all it
+// can at once: a thread's record values are on their way before the factors
+// that scale them are known.
+template <int HD>
+__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeArgs a) {
+  constexpr int W = kJoinThreads / 32, U = 16;
+  __shared__ float part[W][2][8];
+  __shared__ float fin[16];  // joined maximum (log2 units) and 1 / sum per head; fin[7]: the flag
+  __shared__ float sums[kJoinThreads];
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, g = a.group;
+  const int pair = static_cast<int>(blockIdx.x) / a.chunks, chunk = static_cast<int>(blockIdx.x) % a.chunks;
+  const int b = pair / a.n_kv, h = pair % a.n_kv;
+  const bool append = a.k_new != nullptr;
+  const float sl = a.scale_log2;
+  constexpr float kLn2 = 0.69314718f;
+  const DecodeReq r = decode_request<HD>(a, b);
+  // the new row's place
+  size_t to = 0;
+  bool bad_page = false;
+  if (append && r.n > 0) {
+    const int page = a.page_table[static_cast<size_t>(b) * a.ppr + r.L / kPage];
+    bad_page = page < 0 || page >= a.num_pages;
+    to = (((static_cast<size_t>(a.layer) * a.num_pages + page) * a.n_kv + h) * kPage + r.L % kPage) * HD;
+  }
+  const size_t hq0 = static_cast<size_t>(b) * a.n_q + h * g;
+  float* score = a.score ? a.score + static_cast<size_t>(pair) * a.max_tokens : nullptr;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int p0 = a.off[b] + h * r.stages;
+  const DecodeShares share(a.off[a.batch], a.warps);
+  const int w0 = r.stages > 0 ? share.warp_of(p0) : 0;
+  const int n_rec = r.stages > 0 ? share.warp_of(p0 + r.stages - 1) - w0 + 1 : 0;
+  const float* ml = a.rec_ml + static_cast<size_t>(w0 + pair) * 16;
+  // this CTA's output elements [e0, e0 + per): a thread has element e and every `parts`-th record from x on
+  const int per = (g * HD + a.chunks - 1) / a.chunks;
+  const int parts = per >= kJoinThreads ? 1 : kJoinThreads / per, e0 = chunk * per, ne = min(per, g * HD - e0);
+  float s_new = 0.0f;
+  bool reject = r.n == 0 || bad_page;
+#pragma unroll 1
+  for (int eb = 0; eb < max(1, ne); eb += kJoinThreads) {
+    const int x = per >= kJoinThreads ? 0 : t / per, el = per >= kJoinThreads ? eb + t : t % per;
+    const bool mine = el < ne && x < parts;
+    const int e = min(e0 + max(0, min(el, ne - 1)), g * HD - 1), j = e / HD;
+    const float* ro = a.rec_o + static_cast<size_t>(w0 + pair) * g * HD + e;
+    float v[U], mv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = x + u * parts;
+      const bool in = mine && i < n_rec;
+      v[u] = in ? __ldcg(ro + static_cast<size_t>(i) * g * HD) : 0.0f;
+      mv[u] = in ? __ldcg(ml + i * 16 + j) : -INFINITY;
+    }
+    if (eb == 0) {
+      if (n_rec > 0) {
+        // lane = (record mod 4, head), the warps in turn
+        const int hj = lane & 7;
+        float m = -INFINITY, l = 0.0f;
+#pragma unroll 4
+        for (int i = warp * 4 + (lane >> 3); i < n_rec; i += W * 4) {
+          const float mi = __ldcg(ml + i * 16 + hj), li = __ldcg(ml + i * 16 + 8 + hj);
+          const float mn = fmaxf(m, mi), base = log2_base(mn, sl);
+          l = hj == 7 ? l + li : l * rescale(m, sl, base) + li * rescale(mi, sl, base);
+          m = mn;
+        }
+#pragma unroll
+        for (int w = 8; w < 32; w <<= 1) {
+          const float mo = __shfl_xor_sync(0xFFFFFFFFu, m, w), lo = __shfl_xor_sync(0xFFFFFFFFu, l, w);
+          const float mn = fmaxf(m, mo), base = log2_base(mn, sl);
+          l = hj == 7 ? l + lo : l * rescale(m, sl, base) + lo * rescale(mo, sl, base);
+          m = mn;
+        }
+        if (lane < 8) {
+          part[warp][0][lane] = m;
+          part[warp][1][lane] = l;
+        }
+        __syncthreads();
+        if (t < 8) {
+          float mj = -INFINITY, lj = 0.0f;
+#pragma unroll
+          for (int w = 0; w < W; ++w) mj = fmaxf(mj, part[w][0][t]);
+          const float base = log2_base(mj, sl);
+#pragma unroll
+          for (int w = 0; w < W; ++w) lj += t == 7 ? part[w][1][t] : part[w][1][t] * rescale(part[w][0][t], sl, base);
+          fin[t] = t == 7 ? lj : base;
+          fin[8 + t] = 1.0f / lj;
+        }
+      } else if (t < 8) {
+        fin[t] = 0.0f;
+        fin[8 + t] = 1.0f;
+      }
+      __syncthreads();
+      const bool flag = n_rec > 0 && fin[7] != 0.0f;
+      if (chunk == 0 && t == 0) {
+        if (!r.valid && r.L != kIdleSlot) atomicOr(a.status, VSD_DEV_BAD_SEQLEN);
+        if (flag || bad_page) atomicOr(a.status, VSD_DEV_BAD_PAGE);
+      }
+      reject = reject || flag;
+    }
+    const float base = fin[j];
+    float acc = 0.0f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) acc += v[u] * rescale(mv[u], sl, base);
+    if (mine)
+#pragma unroll 4
+      for (int i = x + U * parts; i < n_rec; i += parts)
+        acc += __ldcg(ro + static_cast<size_t>(i) * g * HD) * rescale(__ldcg(ml + i * 16 + j), sl, base);
+    if (parts > 1) {
+      sums[t] = acc;
+      __syncthreads();
+      if (x == 0)
+        for (int y = 1; y < parts; ++y) acc += sums[y * per + t];
+    }
+    if (mine && x == 0) {
+      acc *= fin[8 + j];
+      if (n_rec == 0 && !reject) acc = __bfloat162float(a.v_new[static_cast<size_t>(pair) * HD + e % HD]);  // the new row is all
+      a.out[hq0 * HD + e] = __float2half_rn(reject ? 0.0f : acc);  // one rounding, to the GEMM input type
+    }
+  }
+  if (chunk == 0 && warp == 0) {
+    const int head = lane >> 2, quad = lane & 3;
+    if (append && !reject) {
+      s_new = new_row_score<HD>(a, b, h, head, quad);
+      if (lane < HD / 4) {  // 16 bytes each: K, then V
+        const bool is_v = lane >= HD / 8;
+        const int c = lane % (HD / 8);
+        reinterpret_cast<uint4*>((is_v ? a.v_pool : a.k_pool) + to)[c] =
+            reinterpret_cast<const uint4*>((is_v ? a.v_new : a.k_new) + static_cast<size_t>(pair) * HD)[c];
+      }
+      if (score) {
+        float p = head < g ? (n_rec > 0 ? ex2(fmaf(s_new, sl, -fin[head])) * fin[8 + head] : 1.0f) : 0.0f;
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) p += __shfl_xor_sync(0xFFFFFFFFu, p, w);
+        if (lane == 0) score[r.L] = p;
+      }
+    }
+    if (a.lse && head < g && quad == 0)
+      a.lse[hq0 + head] = reject ? -INFINITY : n_rec > 0 ? (fin[head] - log2f(fin[8 + head])) * kLn2 : s_new * (sl * kLn2);
+  }
+  if (score && !reject && n_rec > 0) {
+    const float* raw = a.raw + hq0 * a.max_tokens;
+    // this CTA's rows, two a thread at a time
+    const int rows = r.L - r.lo, share_rows = ((rows + a.chunks - 1) / a.chunks + 31) / 32 * 32;
+    const int lo = r.lo + chunk * share_rows, hi = min(r.L, lo + share_rows);
+#pragma unroll 1
+    for (int y0 = lo + t; y0 < hi; y0 += 2 * kJoinThreads) {
+      const int y1 = y0 + kJoinThreads;
+      const float old0 = score[y0], old1 = y1 < hi ? score[y1] : 0.0f;
+      float s0[kMaxGroup], s1[kMaxGroup], sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kMaxGroup; ++j) {
+        s0[j] = j < g ? __ldcg(raw + static_cast<size_t>(j) * a.max_tokens + y0) : 0.0f;
+        s1[j] = j < g && y1 < hi ? __ldcg(raw + static_cast<size_t>(j) * a.max_tokens + y1) : 0.0f;
+      }
 #pragma unroll
       for (int j = 0; j < kMaxGroup; ++j)
-        if (j < g) sum += exp2f(s[j] - mj[j]) / lj[j];
-      if (lane == 0) score[i] = (append && i == L) ? sum : score[i] + sum;
-    }
-  }
-  if (append) {
-    const size_t to = row_offset(L);
-    for (int d = threadIdx.x; d < HD; d += kDecodeThreads) {
-      a.k_pool[to + d] = a.k_new[new_off + d];
-      a.v_pool[to + d] = a.v_new[new_off + d];
+        if (j < g) {
+          sum0 += ex2(fmaf(s0[j], sl, -fin[j])) * fin[8 + j];
+          sum1 += ex2(fmaf(s1[j], sl, -fin[j])) * fin[8 + j];
+        }
+      score[y0] = old0 + sum0;
+      if (y1 < hi) score[y1] = old1 + sum1;
     }
   }
 }

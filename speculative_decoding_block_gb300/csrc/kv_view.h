@@ -1,6 +1,5 @@
 // kv_view.h -- what the single-token serving operators (decode attention,
-// eviction) need of a cache object: its shape, its device memory and the
-// tensor maps of its pools.
+// eviction) need of a cache object: its shape and its device memory.
 #pragma once
 
 #include "vsd_common.cuh"
@@ -14,7 +13,11 @@ struct KvView {
   __nv_bfloat16 *k_pool, *v_pool;  // [layers][num_pages][n_kv][16][hd]
   const int* page_table;           // [max_batch][ppr]
   int* status;
-  CUtensorMap tm_k, tm_v;  // rows of the pools, boxes of 16 rows x 64 columns, 128-byte swizzle
+  // attention workspace (shared with the step): partial outputs, their maxima and sums
+  float *ws_o, *ws_ml;
+  int* ws_off;    // [max_batch + 1] first piece of work of each request of the decode attention
+  float* ws_raw;  // scores of the decode attention [max_batch][n_q][max_tokens]
+  size_t ws_floats_o, ws_floats_ml;
 };
 KvView kv_view(const vsd_kv* kv);
 

@@ -1,6 +1,7 @@
 // serve.cu -- host side of the single-token serving operators: decode
 // attention over the paged cache, eviction by accumulated attention weight,
 // and token sampling.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -8,6 +9,7 @@
 #include "evict.cuh"
 #include "host_util.h"
 #include "kv_view.h"
+#include "launch.h"
 #include "sample.cuh"
 
 using namespace vsd;
@@ -19,6 +21,26 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;
+}
+
+template <int HD>
+vsd_status launch_decode(const KvView& c, DecodeArgs& a, cudaStream_t st) {
+  // no more CTAs than one stage per warp could use
+  const int64_t stages = static_cast<int64_t>(a.batch) * c.n_kv * ceil_div_h(c.max_tokens, dec_stage_rows(HD));
+  const int grid = static_cast<int>(std::min<int64_t>(c.sms, std::max<int64_t>(1, (stages + kDecWarps - 1) / kDecWarps)));
+  const int64_t records = static_cast<int64_t>(grid) * kDecWarps + static_cast<int64_t>(a.batch) * c.n_kv;
+  if (records * a.group * HD > static_cast<int64_t>(c.ws_floats_o) || records * 16 > static_cast<int64_t>(c.ws_floats_ml))
+    return fail(VSD_ERR_UNSUPPORTED, "attention workspace too small");
+  const int pairs = a.batch * c.n_kv;
+  a.warps = grid * kDecWarps;
+  a.chunks = std::max(1, std::min(64, 2 * c.sms / pairs));
+  auto* stream = decode_stream_kernel<HD>;
+  const int smem = kDecWarps * kDecStages * kDecStageBytes;
+  CK(ensure_smem_opt_in(reinterpret_cast<const void*>(stream), smem));
+  CK(launch_ex(stream, dim3(grid), dim3(kDecThreads), smem, st, use_pdl(st), false, a));
+  // programmatic dependent launch on any stream: the join waits for the kernel before it, the only thing it depends on
+  CK(launch_ex(decode_join_kernel<HD>, dim3(pairs * a.chunks), dim3(kJoinThreads), 0, st, true, false, a));
+  return VSD_OK;
 }
 
 }  // namespace
@@ -42,6 +64,7 @@ vsd_status vsd_decode_attention(const vsd_model* m, vsd_kv* kv, int32_t layer, i
   if (c.model != m) return fail(VSD_ERR_ARG, "the cache was created for another model");
   if (batch < 1 || batch > c.max_batch || layer < 0 || layer >= c.layers)
     return fail(VSD_ERR_ARG, "batch or layer out of range");
+  if (batch > kDecMaxReqs) return fail(VSD_ERR_UNSUPPORTED, "at most %d requests per call", kDecMaxReqs);
   if (window < 0) return fail(VSD_ERR_ARG, "window %d below 0", window);
   if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(out))
     return fail(VSD_ERR_ARG, "q, k_new, v_new and out must be 16-byte aligned");
@@ -66,13 +89,13 @@ vsd_status vsd_decode_attention(const vsd_model* m, vsd_kv* kv, int32_t layer, i
   a.out = reinterpret_cast<__half*>(out);
   a.lse = lse;
   a.score = score;
+  a.rec_o = c.ws_o;
+  a.rec_ml = c.ws_ml;
+  a.off = c.ws_off;
+  a.raw = c.ws_raw;
   a.status = c.status;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int grid = batch * c.n_kv;
-  if (c.hd == 64) decode_attention_kernel<64><<<grid, kDecodeThreads, 0, st>>>(a);
-  else decode_attention_kernel<128><<<grid, kDecodeThreads, 0, st>>>(a);
-  CK(cudaGetLastError());
-  return VSD_OK;
+  return c.hd == 64 ? launch_decode<64>(c, a, reinterpret_cast<cudaStream_t>(stream))
+                    : launch_decode<128>(c, a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 vsd_status vsd_kv_evict(vsd_kv* kv, int32_t batch, const int32_t* seq_lens, int32_t* new_lens, float* score,
