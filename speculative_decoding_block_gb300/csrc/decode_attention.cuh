@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_stream_kernel(const Dec
   constexpr int RC = HD / 8;              // 16-byte chunks of a row
   constexpr uint32_t BOX = kPage * 128;   // bytes of a block of 16 rows of 128, 128-byte swizzled
   constexpr uint32_t VOFF = kDecStageBytes / 2;
-  extern __shared__ __align__(1024) uint8_t smem[];  // the rings
+  extern __shared__ __align__(1024) uint8_t decode_smem[];  // the rings
   __shared__ int off[kDecMaxReqs + 1];
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, head = lane >> 2, quad = lane & 3;
   const int g = a.group;
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_stream_kernel(const Dec
   const DecodeShares share(off[a.batch], a.warps);
   if (gw >= share.warps || off[a.batch] == 0) return;
   const int it0 = share.first(gw), it1 = share.first(gw + 1);
-  const uint32_t ring_u = smem_u32(smem + warp * kDecStages * kDecStageBytes);
+  const uint32_t ring_u = smem_u32(decode_smem + warp * kDecStages * kDecStageBytes);
   const uint64_t pol = policy_evict_first();
 
 #pragma unroll 1

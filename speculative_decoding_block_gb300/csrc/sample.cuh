@@ -9,8 +9,25 @@
 // id whose cumulative kept mass reaches u times the total.
 //
 // A token id has to be the one that the definition gives, whatever the order
-// of summation, so weights are integers of 2^-44 (sums below 2^18 tokens stay
-// under 2^62) and every sum is exact.
+// of summation, so weights are integers (2^-44 of a power of two above the
+// largest; 2^18 of them stay under 2^63) and every sum is exact.  Their
+// relative error has to be far below a token's share of a 150,000-token row,
+// which float32 is not: with c = 32 / (T ln 2) in two floats, x c = N + f,
+// 2^(N / 32) from a table of 32 pairs and an exponent, exp(f ln 2 / 32) by its
+// series in pairs, about 2^-37 in 45 float32 instructions (float64 runs at a
+// fiftieth of their rate here).
+//
+// Rows without filters (sample_plain_kernel) are streamed once; each tile of
+// 512 tokens leaves its sum, against a power of two of its own, and the tile
+// that holds the sampled mass is read again.
+//
+// With filters (sample_logits_kernel) a row's logits are read once into the
+// shared memory of a cluster of CTAs.  A histogram of their distance from the
+// maximum (counts, merged through distributed shared memory) bounds the
+// tokens that can be kept; where they are few (1024: nearly always), they are
+// gathered in id order in one CTA, which finishes the row alone -- a cluster
+// barrier costs about a microsecond, a block's barrier a twentieth.  Else the
+// thresholds are found by 11-bit digits of the ordered key over the cluster.
 #pragma once
 
 #include "vsd_common.cuh"
@@ -24,6 +41,7 @@ struct SampleRowArgs {
   const float* logits;  // [rows][ld]
   long long ld;
   int rows, vocab;
+  int cs, per;               // CTAs per row, tokens per CTA (a multiple of 4)
   const float* temperature;  // [rows] or nullptr (1)
   const int* top_k;          // [rows] or nullptr (off)
   const float* top_p;        // [rows] or nullptr (off)
@@ -42,212 +60,868 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
 
-constexpr int kSampleThreads = 512;
+// 2^(i / 32) as pairs.
+__device__ const float2 kPow32[32] = {
+    {0x1.0000000000000p+0f, 0x0.0p+0f}, {0x1.059b0e0000000p+0f, -0x1.9d4f520000000p-25f}, {0x1.0b55860000000p+0f, 0x1.9f31220000000p-25f},
+    {0x1.11301e0000000p+0f, -0x1.fdb4960000000p-25f}, {0x1.172b840000000p+0f, -0x1.c157420000000p-27f}, {0x1.1d48740000000p+0f, -0x1.d2e8ca0000000p-25f},
+    {0x1.2387a60000000p+0f, 0x1.ceac480000000p-25f}, {0x1.29e9e00000000p+0f, -0x1.5c04240000000p-25f}, {0x1.306fe00000000p+0f, 0x1.4636e20000000p-25f},
+    {0x1.371a740000000p+0f, -0x1.18aac60000000p-25f}, {0x1.3dea640000000p+0f, 0x1.8246840000000p-25f}, {0x1.44e0860000000p+0f, 0x1.8624b40000000p-30f},
+    {0x1.4bfdae0000000p+0f, -0x1.593abc0000000p-25f}, {0x1.5342b60000000p+0f, -0x1.2c56100000000p-25f}, {0x1.5ab07e0000000p+0f, -0x1.5bd5ec0000000p-27f},
+    {0x1.6247ec0000000p+0f, -0x1.f8b5500000000p-25f}, {0x1.6a09e60000000p+0f, 0x1.9fcef40000000p-26f}, {0x1.71f75e0000000p+0f, 0x1.1d8bee0000000p-25f},
+    {0x1.7a11480000000p+0f, -0x1.829fd00000000p-25f}, {0x1.82589a0000000p+0f, -0x1.accc7c0000000p-26f}, {0x1.8ace540000000p+0f, 0x1.15506e0000000p-27f},
+    {0x1.93737c0000000p+0f, -0x1.e647440000000p-25f}, {0x1.9c49180000000p+0f, 0x1.51f8480000000p-27f}, {0x1.a5503c0000000p+0f, -0x1.b83b540000000p-25f},
+    {0x1.ae89fa0000000p+0f, -0x1.a94b140000000p-26f}, {0x1.b7f7700000000p+0f, -0x1.a094380000000p-25f}, {0x1.c199be0000000p+0f, -0x1.3d56b20000000p-27f},
+    {0x1.cb720e0000000p+0f, -0x1.8837cc0000000p-27f}, {0x1.d5818e0000000p+0f, -0x1.822dbc0000000p-27f}, {0x1.dfc9740000000p+0f, -0x1.908c940000000p-25f},
+    {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}, {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f}};
 
-// One CTA per row, the logits re-read (from L2) by each pass.
-__global__ void __launch_bounds__(kSampleThreads) sample_logits_kernel(const SampleRowArgs a) {
+// A row's weights.
+struct RowWeights {
+  float sh, low;   // x' = max(x - sh, low)
+  float ch, cl;    // c = 32 / (T ln 2)
+  float mo;        // N of the power of two next to the largest weight
+  int n_off;       // bits of the rounding constant plus that N
+};
+constexpr float kRoundMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer
+
+// c, capped where 1 / T leaves float32: no two different logits share the mass at one end, all share it at the other.
+__device__ __forceinline__ double temperature_scale(float T) {
+  return fmin(fmax(46.166241308446828 / static_cast<double>(T), 1e-30), 1e30);
+}
+
+// x c must round to an integer below 2^22; beyond that only logits within a
+// factor of two of the maximum have weight, and their difference from it is exact.
+__device__ __forceinline__ bool needs_shift(float mx, float ch) { return !(fabsf(mx) * ch < 2097152.0f); }
+
+// Weights for logits up to mx (shifted by sh); drop = 1600 / c: that far below, a weight of 2^-50 is nothing.
+__device__ __forceinline__ RowWeights row_weights(float mx, float ch, float cl, float sh, float drop) {
+  RowWeights r;
+  r.ch = ch;
+  r.cl = cl;
+  r.sh = sh;
+  const float m = mx - sh;
+  r.low = fmaxf(m - drop, -3.0e38f);
+  r.mo = floorf(m * ch * (1.0f / 32.0f)) * 32.0f + 32.0f;  // weights below 1 (and a little)
+  r.n_off = __float_as_int(kRoundMagic) + static_cast<int>(r.mo);
+  return r;
+}
+
+// ceil(share * total), exactly; share in [0, 1] (NaN counts as 0).
+__device__ __forceinline__ unsigned long long share_of(unsigned long long total, float share) {
+  if (!(share > 0.0f)) return 0;
+  if (share >= 1.0f) return total;
+  const uint32_t bits = __float_as_uint(share), e = bits >> 23;
+  const unsigned long long m = (bits & 0x7FFFFFu) | (e ? 0x800000u : 0u);
+  const int s = 150 - static_cast<int>(e ? e : 1u);  // share = m 2^-s, s >= 24
+  const unsigned long long hi = __umul64hi(total, m), lo = total * m;
+  if (s >= 88) return total != 0;  // the product is below 2^88
+  unsigned long long q, rest;
+  if (s < 64) {
+    q = (hi << (64 - s)) | (lo >> s);
+    rest = lo << (64 - s);
+  } else {
+    q = hi >> (s - 64);
+    rest = (s > 64 ? hi << (128 - s) : 0) | lo;
+  }
+  return q + (rest != 0);
+}
+
+// Weight of logit x, in 2^-44; tab: this lane's column of the table.
+__device__ __forceinline__ unsigned long long row_weight(const RowWeights& r, float x, const float2* tab) {
+  x = fmaxf(x - r.sh, r.low);  // NaN and -inf come out as nothing
+  const float uh = __fmul_rn(x, r.ch);  // not to be contracted into the sums below
+  const float ul = fmaf(x, r.cl, fmaf(x, r.ch, -uh));
+  const float tm = uh + kRoundMagic;
+  const float f0 = uh - (tm - kRoundMagic);
+  const float f = f0 + ul, fl = ul - (f - f0);  // ul reaches 2^-3 where x c reaches 2^21
+  // z = (f + fl) ln 2 / 32
+  constexpr float kh = 0x1.62e4300000000p-6f, kl = -0x1.05c6100000000p-34f;
+  const float zh = f * kh;
+  const float zl = fmaf(fl, kh, fmaf(f, kl, fmaf(f, kh, -zh)));
+  const float q = zh * zh * fmaf(zh, fmaf(zh, 1.0f / 24.0f, 1.0f / 6.0f), 0.5f);
+  const float sl = zl + q;
+  const int n = __float_as_int(tm) - r.n_off;
+  const float2 t2 = tab[(n & 31) * 32];
+  const float sc = __int_as_float(((n >> 5) + 127) << 23);
+  const float ph = t2.x * zh;
+  const float pl = fmaf(t2.x, sl, fmaf(t2.y, zh, t2.y) + fmaf(t2.x, zh, -ph));
+  // (t + ph + pl) 2^k as integers of 2^-22 and 2^-44
+  const float h = t2.x * sc, p = ph * sc, l = pl * sc;
+  const float e1 = p + l;
+  const float eh = h + e1;
+  const float el = (e1 - (eh - h)) + (l - (e1 - p));
+  const float i1 = eh + 2.0f;
+  const float i2 = ((eh - (i1 - 2.0f)) + el) + 0x1.8p-21f;
+  const int a = __float_as_int(i1) - __float_as_int(2.0f), b = __float_as_int(i2) - __float_as_int(0x1.8p-21f);
+  return (static_cast<unsigned long long>(static_cast<unsigned int>(a)) << 22) + static_cast<long long>(b);
+}
+
+// log of logit x's share of a mass (by one thread of a row: float64).
+__device__ __forceinline__ float log_share(const RowWeights& r, float x, float T, unsigned long long total) {
+  const double z = (static_cast<double>(x) - static_cast<double>(r.sh)) * temperature_scale(T) - static_cast<double>(r.mo);
+  return static_cast<float>(z * 0.021660849392498290 - log(static_cast<double>(total) * (1.0 / static_cast<double>(1ull << kWeightBits))));
+}
+
+constexpr int kSampleThreads = 512;
+constexpr int kSampleBins = 2048;
+constexpr int kSampleMaxCluster = 8;
+constexpr int kSampleList = 1024;  // two entries a thread
+
+// Behind the row's slice.
+struct alignas(16) SampleShared {
+  float2 tab[32 * 32];                    // [entry][lane]: no bank conflicts
+  unsigned long long mass[kSampleBins];   // histogram (counts in the low words where only they are needed)
+  unsigned long long xch[2][kSampleMaxCluster];  // a value of each rank
+  unsigned long long red[kSampleThreads / 32];
+  unsigned long long found[3];            // what the rank that holds a border says
+  float scale[2];                         // c of the row
+};
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_dsmem_u64(uint32_t addr, unsigned long long v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ unsigned long long ld_dsmem_u64(uint32_t addr) {
+  unsigned long long v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(kSampleThreads, 2) sample_logits_kernel(const SampleRowArgs a) {
   constexpr int W = kSampleThreads / 32;
-  __shared__ unsigned long long red[W];
-  __shared__ int hist[256];
-  __shared__ unsigned long long mass[256];
-  __shared__ uint32_t s_key;
-  __shared__ int s_need, s_tok;
-  __shared__ unsigned long long s_left;
-  const int row = blockIdx.x, t = threadIdx.x, warp = t >> 5, lane = t & 31, V = a.vocab;
-  const float* x = a.logits + row * a.ld;
-  auto block_sum = [&](unsigned long long v) {
+  extern __shared__ __align__(16) uint8_t sample_smem[];
+  SampleShared& sh = *reinterpret_cast<SampleShared*>(sample_smem);
+  float* xs = reinterpret_cast<float*>(sample_smem + sizeof(SampleShared));
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, cs = a.cs;
+  const int row = static_cast<int>(blockIdx.x) / cs, rank = static_cast<int>(blockIdx.x) % cs;
+  const int id0 = min(a.vocab, rank * a.per), n = min(a.vocab, id0 + a.per) - id0;
+  const float* src = a.logits + row * a.ld + id0;
+  const float T = a.temperature ? a.temperature[row] : 1.0f;
+  if (cs > 1) cluster_arrive();  // the others' memory is touched once all have started
+  const float2* tab = sh.tab + lane;
+
+  // every rank's value of v (of thread 0), for all threads of all ranks; two buffers in turn
+  int turn = 0;
+  auto exchange = [&](unsigned long long v) -> const unsigned long long* {
+    turn ^= 1;
+    if (cs > 1) {
+      if (t < cs) st_dsmem_u64(mapa_shared(smem_u32(&sh.xch[turn][rank]), t), v);
+      cluster_sync();
+    } else {
+      if (t == 0) sh.xch[turn][0] = v;
+      __syncthreads();
+    }
+    return sh.xch[turn];
+  };
+  auto sync_all = [&]() {
+    if (cs > 1) cluster_sync();
+    else __syncthreads();
+  };
+  auto warp_sum64 = [&](unsigned long long v) {
+#pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    __syncthreads();
-    if (lane == 0) red[warp] = v;
-    __syncthreads();
-    v = 0;
-    for (int w = 0; w < W; ++w) v += red[w];
     return v;
   };
-  // the largest logit, lowest id first
+  // sum over the CTA's threads, and the sum over the threads before this one
+  auto block_scan = [&](unsigned long long v, unsigned long long* before) {
+    unsigned long long c = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, c, o);
+      if (lane >= o) c += y;
+    }
+    __syncthreads();
+    if (lane == 31) sh.red[warp] = c;
+    __syncthreads();
+    unsigned long long pre = 0, all = 0;
+#pragma unroll 1
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) pre += sh.red[w];
+      all += sh.red[w];
+    }
+    *before = pre + c - v;
+    return all;
+  };
+
+  // ------------------------------------------------------------------ the slice, and the largest logit (lowest id first)
   unsigned long long best = 0;
-  for (int i = t; i < V; i += kSampleThreads) {
-    const uint32_t k = logit_key(x[i]);
-    if (k) best = max(best, (static_cast<unsigned long long>(k) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(i)));
+  auto look = [&](float x, int i) {
+    const uint32_t k = logit_key(x);
+    if (k) {
+      const unsigned long long v = (static_cast<unsigned long long>(k) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id0 + i));
+      best = v > best ? v : best;
+    }
+  };
+  {
+    // 16-byte loads from the first aligned address on; xs shifted alike
+    const int head = min(n, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(src) & 15)) & 15) / 4);
+    xs += (4 - head) & 3;
+    const int n4 = (n - head) / 4;
+    const float4* s4 = reinterpret_cast<const float4*>(src + head);
+    float4* d4 = reinterpret_cast<float4*>(xs + head);
+#pragma unroll 1
+    for (int i0 = t; i0 < n4; i0 += 4 * kSampleThreads) {
+      float4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i0 + u * kSampleThreads < n4) v[u] = __ldcs(s4 + i0 + u * kSampleThreads);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * kSampleThreads;
+        if (i < n4) {
+          d4[i] = v[u];
+          look(v[u].x, head + 4 * i);
+          look(v[u].y, head + 4 * i + 1);
+          look(v[u].z, head + 4 * i + 2);
+          look(v[u].w, head + 4 * i + 3);
+        }
+      }
+    }
+    for (int i = t; i < 32 * 32; i += kSampleThreads) sh.tab[i] = kPow32[i >> 5];
+    if (t == kSampleThreads - 1) {
+      const double c = temperature_scale(T);
+      sh.scale[0] = static_cast<float>(c);
+      sh.scale[1] = static_cast<float>(c - static_cast<double>(sh.scale[0]));
+    }
+    const int rest = n - head - 4 * n4;  // and the ragged ends
+    if (t < head + rest) {
+      const int i = t < head ? t : head + 4 * n4 + t - head;
+      const float x = src[i];
+      xs[i] = x;
+      look(x, i);
+    }
   }
-  for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
-  if (lane == 0) red[warp] = best;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const unsigned long long y = __shfl_xor_sync(0xFFFFFFFFu, best, o);
+    best = y > best ? y : best;
+  }
+  if (lane == 0) sh.red[warp] = best;
   __syncthreads();
-  best = 0;
-  for (int w = 0; w < W; ++w) best = max(best, red[w]);
-  const float T = a.temperature ? a.temperature[row] : 1.0f;
-  if (best == 0 || !(T > 0.0f)) {
-    if (t == 0) {
+  for (int w = 0; w < W; ++w) best = sh.red[w] > best ? sh.red[w] : best;
+  if (cs > 1) cluster_wait();
+  {
+    const unsigned long long* all = exchange(best);
+    for (int r = 0; r < cs; ++r) best = all[r] > best ? all[r] : best;
+  }
+  if (best == 0 || !(T > 0.0f)) {  // the whole cluster alike
+    if (rank == 0 && t == 0) {
       a.tokens[row] = best ? static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(best)) : -1;
       if (a.logprob) a.logprob[row] = best ? 0.0f : -INFINITY;
     }
     return;
   }
-  const uint32_t max_key = static_cast<uint32_t>(best >> 32);
-  const double mx = key_logit(max_key), inv_t = 1.0 / static_cast<double>(T);
-  auto weight = [&](uint32_t key) -> unsigned long long {
-    if (key == 0) return 0;
-    if (key == max_key) return 1ull << kWeightBits;
-    const double z = (static_cast<double>(key_logit(key)) - mx) * inv_t;
-    if (!(z > -100.0)) return 0;  // far below half a step (also an infinite maximum)
-    return static_cast<unsigned long long>(__double2ll_rn(exp(z) * static_cast<double>(1ull << kWeightBits)));
-  };
+  uint32_t max_key = static_cast<uint32_t>(best >> 32);
+  if (key_logit(max_key) == INFINITY) {  // the infinite logits share the mass: zeros among nothing
+    for (int i = t; i < n; i += kSampleThreads) xs[i] = xs[i] == INFINITY ? 0.0f : -INFINITY;
+    max_key = logit_key(0.0f);
+    __syncthreads();
+  }
+  const float mx = key_logit(max_key);
+  const RowWeights rw =
+      row_weights(mx, sh.scale[0], sh.scale[1], needs_shift(mx, sh.scale[0]) ? mx : 0.0f, 1600.0f / sh.scale[0]);
+
+  const int top_k = a.top_k ? a.top_k[row] : 0;
+  const float top_p = a.top_p ? a.top_p[row] : 1.0f, min_p = a.min_p ? a.min_p[row] : 0.0f;
+  const bool cut_k = top_k > 0 && top_k < a.vocab, cut_p = top_p < 1.0f;
+  const unsigned long long w_max = row_weight(rw, mx, tab);
+  const unsigned long long floor_w = max(1ull, share_of(w_max, min_p));
+
+  // ------------------------------------------------------------------ the tokens that can be kept, gathered where they are few
+  if (cut_k || cut_p) {
+    // bins of 1/64 below the maximum; the last holds all the rest
+    auto bin_of = [&](float x) { return min(kSampleBins - 1, static_cast<int>((mx - fmaxf(x, -3.0e38f)) * 64.0f)); };
+    uint32_t* count = reinterpret_cast<uint32_t*>(sh.mass);
+    for (int i = t; i < kSampleBins; i += kSampleThreads) count[i] = 0;
+    __syncthreads();
+    unsigned long long sum = 0, before;
+#pragma unroll 1
+    for (int i = t; i < n; i += kSampleThreads) {
+      const float x = xs[i];
+      const int b = bin_of(x);
+      if (b < kSampleBins - 1) atomicAdd(&count[b], 1u);
+      if (!cut_k && logit_key(x)) sum += row_weight(rw, x, tab);
+    }
+    // the goal: k tokens, or p of the row's mass, which tokens of the first bins reach even at their bins' lowest weights
+    unsigned long long goal = static_cast<unsigned long long>(top_k);
+    if (!cut_k) {
+      const unsigned long long own = block_scan(sum, &before);
+      const unsigned long long* all = exchange(own);  // every rank's counts are there, too
+      unsigned long long total = 0;
+      for (int r = 0; r < cs; ++r) total += all[r];
+      goal = max(1ull, share_of(total, top_p));
+    } else {
+      sync_all();
+    }
+    const int mine = kSampleBins / cs, each = max(1, mine / kSampleThreads), b0 = rank * mine + t * each;
+    const float wm = ex2((rw.ch * (mx - rw.sh) - rw.mo) * (1.0f / 32.0f)) * (0.999f * 0x1p44f);
+    auto value = [&](int b) -> unsigned long long {
+      uint32_t c = 0;
+      for (int r = 0; r < cs; ++r) c += __float_as_uint(ld_dsmem_f32(mapa_shared(smem_u32(&count[b]), r)));
+      if (cut_k) return c;
+      const float w = wm * ex2(static_cast<float>(b + 1) * rw.ch * (-1.0f / 2048.0f));
+      return b == 0 ? __float2ull_rd(static_cast<float>(c - 1) * w + wm) : __float2ull_rd(static_cast<float>(c) * w);
+    };
+    sum = 0;
+    if (t * each < mine)
+      for (int e = 0; e < each; ++e) sum += value(b0 + e);
+    const unsigned long long own = block_scan(sum, &before);
+    const unsigned long long* all = exchange(own);
+    unsigned long long total = 0;
+    for (int r = 0; r < cs; ++r) {
+      if (r < rank) before += all[r];
+      total += all[r];
+    }
+    if (total >= goal) {  // the cluster alike: the goal is reached before the last bin
+      if (before < goal && goal <= before + sum) {  // one thread of the cluster
+        int e = 0;
+        for (; e < each - 1; ++e) {
+          before += value(b0 + e);
+          if (goal <= before) break;
+        }
+        for (int r = 0; r < cs; ++r) st_dsmem_u64(mapa_shared(smem_u32(&sh.found[0]), r), static_cast<unsigned long long>(b0 + e));
+      }
+      sync_all();
+      const int border = static_cast<int>(sh.found[0]);
+      // this thread's run of ids (an odd number of them: no bank conflicts), its candidates and their place
+      const int len = ((n + kSampleThreads - 1) / kSampleThreads) | 1, i0 = min(n, t * len), i1 = min(n, i0 + len);
+      int cand = 0;
+      for (int i = i0; i < i1; ++i) cand += bin_of(xs[i]) <= border;
+      unsigned long long at;
+      const unsigned long long mine_c = block_scan(static_cast<unsigned long long>(cand), &at);
+      const unsigned long long* every = exchange(mine_c);
+      unsigned long long cands = 0;
+      for (int r = 0; r < cs; ++r) {
+        if (r < rank) at += every[r];
+        cands += every[r];
+      }
+      if (cands <= kSampleList) {
+        // an entry is larger the earlier its token comes in falling order
+        const uint32_t list_u = mapa_shared(smem_u32(&sh.mass[kSampleBins - kSampleList]), 0);
+        if (cand)
+          for (int i = i0; i < i1; ++i)
+            if (bin_of(xs[i]) <= border)
+              st_dsmem_u64(list_u + 8 * static_cast<uint32_t>(at++),
+                           (static_cast<unsigned long long>(logit_key(xs[i])) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id0 + i)));
+        sync_all();
+        if (rank != 0) return;
+        // ---------------------------------------------------------------- one CTA finishes the row: two entries a thread
+        const unsigned long long* list = &sh.mass[kSampleBins - kSampleList];
+        unsigned long long* hist = sh.mass;                                   // [kSampleList] bins
+        unsigned long long* vals = reinterpret_cast<unsigned long long*>(sample_smem + sizeof(SampleShared));  // [kSampleList]
+        const int N = static_cast<int>(cands);
+        unsigned long long ent[2], w[2];
+        int bin[2];
+        bool keep[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = 2 * t + e;
+          keep[e] = j < N;
+          ent[e] = keep[e] ? list[j] : 0;
+          const float x = key_logit(static_cast<uint32_t>(ent[e] >> 32));
+          w[e] = keep[e] ? row_weight(rw, x, tab) : 0;
+          bin[e] = keep[e] ? bin_of(x) / (kSampleBins / kSampleList) : kSampleList - 1;
+        }
+        // keeps the entries before which (in falling order) less than the goal has been kept: of tokens, or of mass
+#pragma unroll 1
+        for (int step = cut_k ? 0 : 1; step < (cut_p ? 2 : 1); ++step) {
+          const bool by_mass = step == 1;
+          unsigned long long v[2], pre;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) v[e] = !keep[e] ? 0 : by_mass ? w[e] : 1;
+          if (by_mass && cut_k) goal = max(1ull, share_of(block_scan(v[0] + v[1], &pre), top_p));
+          __syncthreads();
+          hist[2 * t] = hist[2 * t + 1] = 0;
+          __syncthreads();
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (v[e]) atomicAdd(&hist[bin[e]], v[e]);
+          __syncthreads();
+          const unsigned long long h0 = hist[2 * t], h1 = hist[2 * t + 1];
+          const unsigned long long in_all = block_scan(h0 + h1, &pre);
+          if (in_all > goal || by_mass) {  // (else every entry stays)
+            if (pre < goal && goal <= pre + h0 + h1) {
+              const bool first = goal <= pre + h0;
+              sh.found[0] = 2 * t + (first ? 0 : 1);
+              sh.found[1] = goal - (first ? pre : pre + h0);
+            }
+            __syncthreads();
+            const int border2 = static_cast<int>(sh.found[0]);
+            const unsigned long long rest = sh.found[1];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) vals[2 * t + e] = bin[e] == border2 ? v[e] : 0;
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (!keep[e]) continue;
+              if (bin[e] == border2) {
+                unsigned long long better = 0;
+                for (int j = 0; j < N; ++j) better += list[j] > ent[e] ? vals[j] : 0;
+                keep[e] = better < rest;
+              } else {
+                keep[e] = bin[e] < border2;
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (!keep[e] || w[e] < floor_w) w[e] = 0;
+        unsigned long long run;
+        const unsigned long long total_w = block_scan(w[0] + w[1], &run);
+        const unsigned long long want = max(1ull, share_of(total_w, a.u[row]));
+        if (run < want && want <= run + w[0] + w[1]) {
+          const int e = want <= run + w[0] ? 0 : 1;
+          a.tokens[row] = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(ent[e]));
+          if (a.logprob) a.logprob[row] = log_share(rw, key_logit(static_cast<uint32_t>(ent[e] >> 32)), T, total_w);
+        }
+        return;
+      }
+    }
+  }
+
+  // ------------------------------------------------------------------ thresholds
   // kept: key > thr, and the first `ties` ids of key == thr
   uint32_t thr = 0;
-  int ties = 0;
-  auto tighten = [&](uint32_t k, int n) {
-    if (k > thr) {
-      thr = k;
-      ties = n;
-    } else if (k == thr) {
-      ties = min(ties, n);
+  int ties = 0, equals = 0;  // equals: how many tokens have that key
+  // Finds the key at which a sum over tokens in falling order reaches a goal: tokens counted (goal = k), or their mass
+  // (goal = p of the mass of those kept so far).
+  auto select = [&](bool by_mass, float share, unsigned long long goal) {
+    uint32_t prefix = 0;
+    const unsigned long long w_thr = by_mass && thr ? row_weight(rw, key_logit(thr), tab) : 0;
+#pragma unroll 1
+    for (int level = 0; level < 3; ++level) {
+      const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11, bins = 1 << bits;
+      for (int i = t; i < bins; i += kSampleThreads) sh.mass[i] = 0;
+      __syncthreads();
+      uint32_t* count = reinterpret_cast<uint32_t*>(sh.mass);
+#pragma unroll 1
+      for (int i = t; i < n; i += kSampleThreads) {
+        const float x = xs[i];
+        const uint32_t k = logit_key(x);
+        if (k == 0 || (level && (k >> (shift + bits)) != (prefix >> (shift + bits)))) continue;
+        const int bin = bins - 1 - ((k >> shift) & (bins - 1));  // largest first
+        if (!by_mass) atomicAdd(&count[bin], 1u);
+        else if (k > thr) atomicAdd(&sh.mass[bin], row_weight(rw, x, tab));
+      }
+      if (by_mass && rank == 0 && t == 0 && thr && (!level || (thr >> (shift + bits)) == (prefix >> (shift + bits))))
+        atomicAdd(&sh.mass[bins - 1 - ((thr >> shift) & (bins - 1))], w_thr * static_cast<unsigned long long>(ties));
+      sync_all();
+      // this rank's share of the bins, over all ranks
+      const int mine = bins / cs, each = max(1, mine / kSampleThreads), b0 = rank * mine + t * each;
+      unsigned long long sum = 0, before;
+      if (t * each < mine)
+        for (int e = 0; e < each; ++e)
+          for (int r = 0; r < cs; ++r)
+            sum += by_mass ? ld_dsmem_u64(mapa_shared(smem_u32(&sh.mass[b0 + e]), r))
+                           : __float_as_uint(ld_dsmem_f32(mapa_shared(smem_u32(&count[b0 + e]), r)));
+      const unsigned long long own = block_scan(sum, &before);
+      const unsigned long long* all = exchange(own);
+      unsigned long long total = 0;
+      for (int r = 0; r < cs; ++r) {
+        if (r < rank) before += all[r];
+        total += all[r];
+      }
+      if (level == 0) {
+        if (by_mass) goal = max(1ull, share_of(total, share));
+        else if (goal >= total) return;  // no more tokens than that: nothing to cut
+      }
+      if (before < goal && goal <= before + sum) {  // one thread of the cluster
+        unsigned long long v = 0;
+        int e = 0;
+        for (;; ++e) {
+          v = 0;
+          for (int r = 0; r < cs; ++r)
+            v += by_mass ? ld_dsmem_u64(mapa_shared(smem_u32(&sh.mass[b0 + e]), r))
+                         : __float_as_uint(ld_dsmem_f32(mapa_shared(smem_u32(&count[b0 + e]), r)));
+          if (e == each - 1 || goal <= before + v) break;
+          before += v;
+        }
+        for (int r = 0; r < cs; ++r) {
+          st_dsmem_u64(mapa_shared(smem_u32(&sh.found[0]), r), static_cast<unsigned long long>(b0 + e));
+          st_dsmem_u64(mapa_shared(smem_u32(&sh.found[1]), r), goal - before);
+          st_dsmem_u64(mapa_shared(smem_u32(&sh.found[2]), r), v);
+        }
+      }
+      sync_all();
+      prefix |= static_cast<uint32_t>(bins - 1 - static_cast<int>(sh.found[0])) << shift;
+      goal = sh.found[1];
+    }
+    // of the border's equals, as many as the rest of the goal needs
+    const unsigned long long v = sh.found[2];
+    int need, have;
+    if (by_mass) {
+      const unsigned long long w = row_weight(rw, key_logit(prefix), tab);
+      need = static_cast<int>((goal + w - 1) / w);
+      have = static_cast<int>(v / w);
+    } else {
+      need = static_cast<int>(goal);
+      have = static_cast<int>(v);
+    }
+    if (prefix != thr) {
+      thr = prefix;
+      ties = need;
+      equals = have;
+    } else {
+      ties = min(ties, need);
     }
   };
-  const int top_k = a.top_k ? a.top_k[row] : 0;
-  if (top_k > 0 && top_k < V) {
-    uint32_t prefix = 0;
-    int need = top_k;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      __syncthreads();
-      if (t < 256) hist[t] = 0;
-      __syncthreads();
-      for (int i = t; i < V; i += kSampleThreads) {
-        const uint32_t k = logit_key(x[i]);
-        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255], 1);
-      }
-      __syncthreads();
-      if (t == 0) {
-        int d = 255, left = need;
-        for (; d > 0 && hist[d] < left; --d) left -= hist[d];
-        s_key = prefix | (static_cast<uint32_t>(d) << shift);
-        s_need = left;
-      }
-      __syncthreads();
-      prefix = s_key;
-      need = s_need;
-    }
-    tighten(prefix, need);
-  }
-  const float top_p = a.top_p ? a.top_p[row] : 1.0f;
-  if (top_p < 1.0f) {
-    // mass of the tokens kept so far
-    unsigned long long sum = 0;
-    for (int i = t; i < V; i += kSampleThreads) {
-      const uint32_t k = logit_key(x[i]);
-      if (k > thr) sum += weight(k);
-    }
-    const unsigned long long total = block_sum(sum) + (thr ? static_cast<unsigned long long>(ties) * weight(thr) : 0);
-    // digit by digit: the key at which the mass from the top reaches p * total
-    const double target = fmax(static_cast<double>(top_p), 0.0) * static_cast<double>(total);
-    unsigned long long goal = static_cast<unsigned long long>(ceil(target));
-    if (goal == 0) goal = 1;
-    uint32_t prefix = 0;
-    unsigned long long left = goal;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      __syncthreads();
-      if (t < 256) mass[t] = 0;
-      __syncthreads();
-      for (int i = t; i < V; i += kSampleThreads) {
-        const uint32_t k = logit_key(x[i]);
-        if (k <= thr) continue;
-        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&mass[(k >> shift) & 255], weight(k));
-      }
-      if (t == 0 && thr && (shift == 24 || (thr >> (shift + 8)) == (prefix >> (shift + 8))))
-        atomicAdd(&mass[(thr >> shift) & 255], static_cast<unsigned long long>(ties) * weight(thr));
-      __syncthreads();
-      if (t == 0) {
-        int d = 255;
-        unsigned long long l = left;
-        for (; d > 0 && mass[d] < l; --d) l -= mass[d];
-        s_key = prefix | (static_cast<uint32_t>(d) << shift);
-        s_left = l;
-      }
-      __syncthreads();
-      prefix = s_key;
-      left = s_left;
-    }
-    const unsigned long long w = weight(prefix);
-    const unsigned long long n = w ? (left + w - 1) / w : static_cast<unsigned long long>(V);
-    tighten(prefix, static_cast<int>(min(n, static_cast<unsigned long long>(V))));
-  }
-  const float min_p = a.min_p ? a.min_p[row] : 0.0f;
-  const unsigned long long floor_w =
-      min_p > 0.0f ? static_cast<unsigned long long>(ceil(fmin(static_cast<double>(min_p), 1.0) * static_cast<double>(1ull << kWeightBits))) : 1ull;
-  // total of the kept tokens, by chunks of consecutive ids: each warp owns a range
-  const int per = (V + W - 1) / W, w0 = min(V, warp * per), w1 = min(V, w0 + per);
+  if (cut_k) select(false, 0.0f, static_cast<unsigned long long>(top_k));
+  if (cut_p) select(true, top_p, 0);
+  const unsigned long long w_thr0 = thr ? row_weight(rw, key_logit(thr), tab) : 0, w_thr = w_thr0 >= floor_w ? w_thr0 : 0;
+  // weight of token i of the slice; ties are left to the caller
+  auto kept_weight = [&](int i, bool* tie) -> unsigned long long {
+    const float x = xs[i];
+    const uint32_t k = logit_key(x);
+    *tie = k && k == thr;
+    if (k <= thr) return 0;
+    const unsigned long long w = row_weight(rw, x, tab);
+    return w >= floor_w ? w : 0;
+  };
+  const bool all_ties = ties >= equals;  // every equal of the threshold stays (or there is none)
+
+  // ------------------------------------------------------------------ total, and the part of the row that holds the goal
+  // Three rounds: the cluster's slices, a warp's part of a slice, a thread's part of that.
+  const int part = (n + W - 1) / W, p0 = min(n, warp * part), p1 = min(n, p0 + part);
   unsigned long long sum = 0;
-  int eq = 0;  // equals of the threshold in this warp's range
-  for (int i = w0 + lane; i < w1; i += 32) {
-    const uint32_t k = logit_key(x[i]);
-    if (k > thr) {
-      const unsigned long long w = weight(k);
-      if (w >= floor_w) sum += w;
-    } else if (k == thr && k) {
-      ++eq;
-    }
+  int eq = 0;
+#pragma unroll 1
+  for (int i = p0 + lane; i < p1; i += 32) {
+    bool tie;
+    sum += kept_weight(i, &tie);
+    eq += tie;
   }
-  for (int o = 16; o > 0; o >>= 1) {
-    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    eq += __shfl_xor_sync(0xFFFFFFFFu, eq, o);
-  }
+  eq = __reduce_add_sync(0xFFFFFFFFu, eq);
+  sum = warp_sum64(sum);
   __syncthreads();
   if (lane == 0) {
-    mass[warp] = sum;
-    hist[warp] = eq;
+    sh.mass[warp] = sum;
+    sh.mass[W + warp] = static_cast<unsigned long long>(eq);
   }
   __syncthreads();
-  const unsigned long long wt0 = weight(thr), wt = wt0 >= floor_w ? wt0 : 0;
-  unsigned long long before = 0, total = 0;
-  int eq_before = 0, eq_all = 0;
+  unsigned long long cta_sum = 0, cta_eq = 0;
   for (int w = 0; w < W; ++w) {
-    const unsigned long long m = mass[w] + wt * static_cast<unsigned long long>(max(0, min(hist[w], ties - eq_all)));
-    if (w < warp) {
-      before += m;
-      eq_before += hist[w];
-    }
-    eq_all += hist[w];
-    total += m;
+    cta_sum += sh.mass[w];
+    cta_eq += sh.mass[W + w];
   }
-  const float uf = a.u[row];
-  unsigned long long goal = static_cast<unsigned long long>(ceil(fmin(fmax(static_cast<double>(uf), 0.0), 1.0) * static_cast<double>(total)));
-  goal = max(1ull, min(goal, total));
-  if (t == 0) s_tok = -1;
-  __syncthreads();
-  // the range that holds the goal: its warp walks it 32 ids at a time
-  const unsigned long long mine =
-      mass[warp] + wt * static_cast<unsigned long long>(max(0, min(hist[warp], ties - eq_before)));
-  if (before < goal && goal <= before + mine) {
-    unsigned long long run = before;
-    int seen = eq_before;
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-      const int i = i0 + lane;
-      const uint32_t k = i < w1 ? logit_key(x[i]) : 0;
-      const bool tie = k && k == thr;
-      const unsigned tb = __ballot_sync(0xFFFFFFFFu, tie);
-      unsigned long long w = 0;
-      if (k > thr) {
-        w = weight(k);
-        if (w < floor_w) w = 0;
-      } else if (tie && seen + __popc(tb & ((1u << lane) - 1)) < ties) {
-        w = wt;
+  // equals before this rank decide how many of its own stay
+  long long eq_before = 0;
+  if (!all_ties) {
+    const unsigned long long* all = exchange(cta_eq);
+    for (int r = 0; r < rank; ++r) eq_before += static_cast<long long>(all[r]);
+  }
+  auto stay = [&](long long seen, unsigned long long here) -> unsigned long long {  // equals that stay, of `here` after `seen`
+    if (all_ties) return here;
+    const long long room = static_cast<long long>(ties) - seen;
+    return room <= 0 ? 0 : min(here, static_cast<unsigned long long>(room));
+  };
+  cta_sum += w_thr * stay(eq_before, cta_eq);
+  unsigned long long run = 0, total = 0;
+  {
+    const unsigned long long* all = exchange(cta_sum);
+    for (int r = 0; r < cs; ++r) {
+      if (r < rank) run += all[r];
+      total += all[r];
+    }
+  }
+  const unsigned long long goal = max(1ull, share_of(total, a.u[row]));
+  if (!(run < goal && goal <= run + cta_sum)) return;  // another CTA's (no rank looks into another's memory from here on)
+  int q0 = 0, q1 = n;
+  long long seen = eq_before;
+#pragma unroll 1
+  for (int w = 0; w < W; ++w) {
+    const unsigned long long m = sh.mass[w] + w_thr * stay(seen, sh.mass[W + w]);
+    if (goal <= run + m) {
+      q0 = min(n, w * part);
+      q1 = min(n, q0 + part);
+      break;
+    }
+    run += m;
+    seen += static_cast<long long>(sh.mass[W + w]);
+  }
+  const int each = (q1 - q0 + kSampleThreads - 1) / kSampleThreads, r0 = min(q1, q0 + t * each), r1 = min(q1, r0 + each);
+  unsigned long long mine = 0, before;
+  int my_eq = 0;
+  for (int i = r0; i < r1; ++i) {
+    bool tie;
+    mine += kept_weight(i, &tie);
+    my_eq += tie;
+  }
+  unsigned long long eq_pre;
+  block_scan(static_cast<unsigned long long>(my_eq), &eq_pre);
+  seen += static_cast<long long>(eq_pre);
+  mine += w_thr * stay(seen, static_cast<unsigned long long>(my_eq));
+  block_scan(mine, &before);
+  run += before;
+  if (run < goal && goal <= run + mine) {
+    for (int i = r0; i < r1; ++i) {
+      bool tie;
+      unsigned long long w = kept_weight(i, &tie);
+      if (tie) {
+        w = w_thr * stay(seen, 1);
+        ++seen;
       }
-      seen += __popc(tb);
-      unsigned long long c = w;
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, c, o);
-        if (lane >= o) c += y;
-      }
-      const unsigned hit = __ballot_sync(0xFFFFFFFFu, w > 0 && run + c >= goal);
-      if (hit) {
-        if (lane == __ffs(hit) - 1) {
-          a.tokens[row] = i;
-          if (a.logprob)
-            a.logprob[row] = static_cast<float>((k == max_key ? 0.0 : (static_cast<double>(key_logit(k)) - mx) * inv_t) -
-                                                log(static_cast<double>(total) / static_cast<double>(1ull << kWeightBits)));
-        }
+      run += w;
+      if (w > 0 && goal <= run) {
+        a.tokens[row] = id0 + i;
+        if (a.logprob) a.logprob[row] = log_share(rw, xs[i], T, total);
         break;
       }
-      run += __shfl_sync(0xFFFFFFFFu, c, 31);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ rows without filters
+constexpr int kPlainThreads = 256;
+constexpr int kPlainTile = 512;  // tokens of a warp's tile
+constexpr int kPlainMaxTiles = kMaxSampleVocab / kPlainTile;
+
+__global__ void __launch_bounds__(kPlainThreads, 4) sample_plain_kernel(const SampleRowArgs a) {
+  constexpr int W = kPlainThreads / 32, E = kPlainTile / 32;
+  __shared__ float2 table[32 * 32];
+  __shared__ unsigned long long tile_sum[kPlainMaxTiles];
+  __shared__ float tile_mo[kPlainMaxTiles];  // the power of two that a tile's sum is against (32nds of an octave)
+  __shared__ unsigned long long xch[3][kSampleMaxCluster], red[W];
+  __shared__ float scale[2];
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, cs = a.cs;
+  const int row = static_cast<int>(blockIdx.x) / cs, rank = static_cast<int>(blockIdx.x) % cs;
+  const int id0 = min(a.vocab, rank * a.per), n = min(a.vocab, id0 + a.per) - id0;
+  const float* src = a.logits + row * a.ld + id0;
+  const float T = a.temperature ? a.temperature[row] : 1.0f;
+  if (cs > 1) cluster_arrive();
+  for (int i = t; i < 32 * 32; i += kPlainThreads) table[i] = kPow32[i >> 5];
+  if (t == 0) {
+    const double c = temperature_scale(T);
+    scale[0] = static_cast<float>(c);
+    scale[1] = static_cast<float>(c - static_cast<double>(scale[0]));
+  }
+  const float2* tab = table + lane;
+  if (cs > 1) cluster_wait();
+  else __syncthreads();
+  __syncthreads();
+  // every rank's value, for all threads of all ranks; buffers in turn
+  auto exchange = [&](int buf, unsigned long long v) -> const unsigned long long* {
+    if (cs > 1) {
+      if (t < cs) st_dsmem_u64(mapa_shared(smem_u32(&xch[buf][rank]), t), v);
+      cluster_sync();
+    } else {
+      if (t == 0) xch[buf][0] = v;
+      __syncthreads();
+    }
+    return xch[buf];
+  };
+  auto block_max = [&](unsigned long long v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const unsigned long long y = __shfl_xor_sync(0xFFFFFFFFu, v, o);
+      v = y > v ? y : v;
+    }
+    __syncthreads();
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    for (int w = 0; w < W; ++w) v = red[w] > v ? red[w] : v;
+    return v;
+  };
+  const int tiles = (n + kPlainTile - 1) / kPlainTile;
+  const bool aligned = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+  auto load = [&](int q, float* x) {
+    const int base = q * kPlainTile;
+    if (aligned && base + kPlainTile <= n) {
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(src + base) + (e / 4) * 32 + lane);
+        x[e] = v.x;
+        x[e + 1] = v.y;
+        x[e + 2] = v.z;
+        x[e + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int i = base + e * 32 + lane;
+        x[e] = i < n ? src[i] : -INFINITY;
+      }
+    }
+  };
+  // id within the slice of element e of tile q as load() deals them
+  auto id_of = [&](int q, int e) {
+    const int base = q * kPlainTile;
+    return base + (aligned && base + kPlainTile <= n ? ((e / 4) * 32 + lane) * 4 + (e & 3) : e * 32 + lane);
+  };
+  if (!(T > 0.0f)) {  // the largest logit, lowest id first
+    unsigned long long best = 0;
+    for (int q = warp; q < tiles; q += W) {
+      float x[E];
+      load(q, x);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint32_t k = logit_key(x[e]);
+        const unsigned long long v =
+            k ? (static_cast<unsigned long long>(k) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id0 + id_of(q, e))) : 0;
+        best = v > best ? v : best;
+      }
+    }
+    best = block_max(best);
+    const unsigned long long* all = exchange(0, best);
+    for (int r = 0; r < cs; ++r) best = all[r] > best ? all[r] : best;
+    if (rank == 0 && t == 0) {
+      a.tokens[row] = best ? static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(best)) : -1;
+      if (a.logprob) a.logprob[row] = best ? 0.0f : -INFINITY;
+    }
+    return;
+  }
+  const float ch = scale[0], cl = scale[1], drop = 1600.0f / ch;
+  // Once over the row; a second time, shifted by the row's maximum, where some tile's values are too large for the first.
+  float shift = 0.0f;
+  bool infinite = false;  // then the infinite logits share the mass: zeros among nothing
+  auto prepared = [&](float x) { return infinite ? (x == INFINITY ? 0.0f : -INFINITY) : fmaxf(x, -INFINITY); };  // NaN: -inf
+  uint32_t top = 0;
+  float mo = 0.0f;
+#pragma unroll 1
+  for (int pass = 0;; ++pass) {
+    uint32_t my_top = 0;
+    bool large = false;
+    float my_mo = -INFINITY;
+#pragma unroll 1
+    for (int q = warp; q < tiles; q += W) {
+      float x[E];
+      load(q, x);
+      float m = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        x[e] = prepared(x[e]);
+        m = fmaxf(m, x[e]);
+      }
+      const uint32_t key = __reduce_max_sync(0xFFFFFFFFu, logit_key(m));
+      const float mx = key_logit(key);
+      my_top = max(my_top, key);
+      unsigned long long sum = 0;
+      float t_mo = -INFINITY;
+      if (key && (mx - shift) * ch > -2097152.0f && !needs_shift(mx - shift, ch)) {
+        const RowWeights rw = row_weights(mx, ch, cl, shift, drop);
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum += row_weight(rw, x[e], tab);
+        t_mo = rw.mo;
+      } else if (key && pass == 0) {
+        large = true;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+      if (lane == 0) {
+        tile_sum[q] = sum;
+        tile_mo[q] = t_mo;
+      }
+      my_mo = fmaxf(my_mo, t_mo);
+    }
+    // (flag, largest key) and the largest power of two
+    const unsigned long long v = block_max((static_cast<unsigned long long>(my_top) << 1) | (large ? 1 : 0));
+    const bool cta_large = __syncthreads_or(large);
+    const unsigned long long* all = exchange(0, (v & ~1ull) | (cta_large ? 1 : 0));
+    bool again = false;
+    top = 0;
+    for (int r = 0; r < cs; ++r) {
+      top = max(top, static_cast<uint32_t>(all[r] >> 1));
+      again = again || (all[r] & 1);
+    }
+    const unsigned long long mv = block_max(my_mo == -INFINITY ? 0 : float_order_key(my_mo));
+    const unsigned long long* mos = exchange(1, mv);
+    uint32_t mk = 0;
+    for (int r = 0; r < cs; ++r) mk = max(mk, static_cast<uint32_t>(mos[r]));
+    mo = key_logit(mk);
+    if (!again || pass == 1 || top == 0) break;
+    shift = key_logit(top);
+    if (shift == INFINITY) {
+      infinite = true;
+      shift = 0.0f;
+    }
+  }
+  if (top == 0) {  // nothing to sample (the cluster alike)
+    if (rank == 0 && t == 0) {
+      a.tokens[row] = -1;
+      if (a.logprob) a.logprob[row] = -INFINITY;
+    }
+    return;
+  }
+  // the tiles' sums against the row's power of two; a run of them per thread, in order
+  auto octaves = [&](int q) { return tile_mo[q] == -INFINITY ? 63 : min(63, static_cast<int>(mo - tile_mo[q]) >> 5); };
+  const int run_len = (tiles + kPlainThreads - 1) / kPlainThreads, q0 = min(tiles, t * run_len), q1 = min(tiles, q0 + run_len);
+  unsigned long long mine = 0;
+  for (int q = q0; q < q1; ++q) mine += tile_sum[q] >> octaves(q);
+  unsigned long long c = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, c, o);
+    if (lane >= o) c += y;
+  }
+  __syncthreads();
+  if (lane == 31) red[warp] = c;
+  __syncthreads();
+  unsigned long long before = c - mine, own = 0;
+  for (int w = 0; w < W; ++w) {
+    if (w < warp) before += red[w];
+    own += red[w];
+  }
+  const unsigned long long* all = exchange(2, own);
+  unsigned long long total = 0;
+  for (int r = 0; r < cs; ++r) {
+    if (r < rank) before += all[r];
+    total += all[r];
+  }
+  const unsigned long long goal = max(1ull, share_of(total, a.u[row]));
+  const bool hit = before < goal && goal <= before + mine;
+  if (!__any_sync(0xFFFFFFFFu, hit)) return;  // (no rank looks into another's memory from here on)
+  // this warp finds the tile, reads it again and finds the token
+  int q = 0;
+  unsigned long long left = 0;
+  if (hit) {
+    for (q = q0; q < q1 - 1; ++q) {
+      const unsigned long long s = tile_sum[q] >> octaves(q);
+      if (goal <= before + s) break;
+      before += s;
+    }
+    left = goal - before;
+  }
+  const int who = __ffs(__ballot_sync(0xFFFFFFFFu, hit)) - 1;
+  q = __shfl_sync(0xFFFFFFFFu, q, who);
+  left = __shfl_sync(0xFFFFFFFFu, left, who);
+  left <<= octaves(q);  // in the tile's own units: at most its sum
+  float x[E], m = -INFINITY;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int i = q * kPlainTile + lane * E + e;
+    x[e] = i < n ? prepared(src[i]) : -INFINITY;
+    m = fmaxf(m, x[e]);
+  }
+  const float mx = key_logit(__reduce_max_sync(0xFFFFFFFFu, logit_key(m)));
+  const RowWeights rw = row_weights(mx, ch, cl, shift, drop);
+  unsigned long long sum = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) sum += row_weight(rw, x[e], tab);
+  unsigned long long pre = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, pre, o);
+    if (lane >= o) pre += y;
+  }
+  pre -= sum;
+  if (pre < left && left <= pre + sum) {
+    int found = 0;
+    float xf = 0.0f;
+    bool done = false;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      pre += row_weight(rw, x[e], tab);
+      if (!done && left <= pre) {
+        done = true;
+        found = e;
+        xf = x[e];
+      }
+    }
+    a.tokens[row] = id0 + q * kPlainTile + lane * E + found;
+    if (a.logprob) {
+      RowWeights rr = rw;
+      rr.mo = mo;
+      a.logprob[row] = log_share(rr, xf, T, total);
     }
   }
 }

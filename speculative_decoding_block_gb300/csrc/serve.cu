@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 
 #include "decode_attention.cuh"
 #include "evict.cuh"
@@ -40,6 +41,30 @@ vsd_status launch_decode(const KvView& c, DecodeArgs& a, cudaStream_t st) {
   CK(launch_ex(stream, dim3(grid), dim3(kDecThreads), smem, st, use_pdl(st), false, a));
   // programmatic dependent launch on any stream: the join waits for the kernel before it, the only thing it depends on
   CK(launch_ex(decode_join_kernel<HD>, dim3(pairs * a.chunks), dim3(kJoinThreads), 0, st, true, false, a));
+  return VSD_OK;
+}
+
+vsd_status launch_sample(SampleRowArgs& a, cudaStream_t st) {
+  int sms = 0, dev = 0;
+  CK(cudaGetDevice(&dev));
+  CK(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  a.cs = 1;
+  if (!a.top_k && !a.top_p && !a.min_p) {
+    static const int want = getenv("SP_W") ? atoi(getenv("SP_W")) : 12;
+    // no filter on any row: streamed; CTAs per row so that the SMs' shares come out even
+    while (a.cs < kSampleMaxCluster && static_cast<int64_t>(a.rows) * a.cs < want * sms && a.vocab > a.cs * 4 * kPlainTile) a.cs *= 2;
+    a.per = ceil_div_h(ceil_div_h(a.vocab, a.cs), kPlainTile) * kPlainTile;
+    CK(launch_ex_cluster(sample_plain_kernel, dim3(static_cast<unsigned>(a.rows) * a.cs), dim3(kPlainThreads), 0, a.cs, st, false, a));
+    return VSD_OK;
+  }
+  static const int fcs = getenv("SP_CS") ? atoi(getenv("SP_CS")) : 0;
+  // CTAs per row: enough for two per SM, and slices that leave room for two (their number, where the row is long)
+  while (a.cs < kSampleMaxCluster && (a.vocab > a.cs * 18000 || (static_cast<int64_t>(a.rows) * a.cs < 2 * sms && a.vocab > a.cs * 1024))) a.cs *= 2;
+  if (fcs) a.cs = fcs;
+  a.per = (ceil_div_h(a.vocab, a.cs) + 3) / 4 * 4;
+  const int smem = static_cast<int>(sizeof(SampleShared)) + std::max((a.per + 4) * 4, kSampleList * 8);
+  CK(ensure_smem_opt_in(reinterpret_cast<const void*>(sample_logits_kernel), smem));
+  CK(launch_ex_cluster(sample_logits_kernel, dim3(static_cast<unsigned>(a.rows) * a.cs), dim3(kSampleThreads), smem, a.cs, st, false, a));
   return VSD_OK;
 }
 
@@ -159,9 +184,7 @@ vsd_status vsd_sample_logits(const float* logits, int32_t rows, int32_t vocab, i
   a.u = u;
   a.tokens = tokens;
   a.logprob = logprob;
-  sample_logits_kernel<<<rows, kSampleThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-  CK(cudaGetLastError());
-  return VSD_OK;
+  return launch_sample(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
