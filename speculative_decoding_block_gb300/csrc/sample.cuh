@@ -161,19 +161,22 @@ __device__ __forceinline__ float log_share(const RowWeights& r, float x, float T
   return static_cast<float>(z * 0.021660849392498290 - log(static_cast<double>(total) * (1.0 / static_cast<double>(1ull << kWeightBits))));
 }
 
-constexpr int kSampleThreads = 512;
+constexpr int kSampleThreads = 1024;
 constexpr int kSampleBins = 2048;
 constexpr int kSampleMaxCluster = 8;
-constexpr int kSampleList = 1024;  // two entries a thread
+constexpr int kSampleList = 1024;  // an entry a thread
 
-// Behind the row's slice.
+// In front of the row's slice.
 struct alignas(16) SampleShared {
-  float2 tab[32 * 32];                    // [entry][lane]: no bank conflicts
-  unsigned long long mass[kSampleBins];   // histogram (counts in the low words where only they are needed)
-  unsigned long long xch[2][kSampleMaxCluster];  // a value of each rank
+  float2 tab[32 * 32];                  // [entry][lane]: no bank conflicts
+  uint32_t hist[4][kSampleBins];        // masses in 16-bit parts (64-bit atomics are loops here), counts
+  unsigned long long list[kSampleList]; // rank 0's: candidates, (key, ~id): larger = earlier in falling order
+  unsigned long long ord[kSampleList], vals[kSampleList];
+  unsigned long long xch[2][kSampleMaxCluster][3];  // values of each rank
   unsigned long long red[kSampleThreads / 32];
-  unsigned long long found[3];            // what the rank that holds a border says
-  float scale[2];                         // c of the row
+  unsigned long long found[4];          // what the thread that holds a border says
+  uint32_t n_list, members;
+  float scale[2];                       // c of the row
 };
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -186,9 +189,36 @@ __device__ __forceinline__ unsigned long long ld_dsmem_u64(uint32_t addr) {
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ uint32_t atom_add_dsmem(uint32_t addr, uint32_t v) {
+  uint32_t old;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(addr), "r"(v) : "memory");
+  return old;
+}
 
-__global__ void __launch_bounds__(kSampleThreads, 2) sample_logits_kernel(const SampleRowArgs a) {
-  constexpr int W = kSampleThreads / 32;
+__device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+// Adds a weight (below 2^48) to a bin; 2^16 weights fit.
+__device__ __forceinline__ void add_mass(uint32_t (*hist)[kSampleBins], int bin, unsigned long long w) {
+  const uint32_t low = static_cast<uint32_t>(w), high = static_cast<uint32_t>(w >> 32);
+  atomicAdd(&hist[0][bin], low & 0xFFFFu);
+  if (low >> 16) atomicAdd(&hist[1][bin], low >> 16);
+  if (high) atomicAdd(&hist[2][bin], high);
+}
+
+// Inclusive sum over the warp's lanes up to this one.
+__device__ __forceinline__ unsigned long long warp_scan(unsigned long long v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+
+__global__ void __launch_bounds__(kSampleThreads, 1) sample_logits_kernel(const SampleRowArgs a) {
   extern __shared__ __align__(16) uint8_t sample_smem[];
   SampleShared& sh = *reinterpret_cast<SampleShared*>(sample_smem);
   float* xs = reinterpret_cast<float*>(sample_smem + sizeof(SampleShared));
@@ -197,60 +227,47 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_logits_kernel(const 
   const int id0 = min(a.vocab, rank * a.per), n = min(a.vocab, id0 + a.per) - id0;
   const float* src = a.logits + row * a.ld + id0;
   const float T = a.temperature ? a.temperature[row] : 1.0f;
+  if (t == 0) sh.n_list = 0;
   if (cs > 1) cluster_arrive();  // the others' memory is touched once all have started
   const float2* tab = sh.tab + lane;
 
-  // every rank's value of v (of thread 0), for all threads of all ranks; two buffers in turn
-  int turn = 0;
-  auto exchange = [&](unsigned long long v) -> const unsigned long long* {
-    turn ^= 1;
-    if (cs > 1) {
-      if (t < cs) st_dsmem_u64(mapa_shared(smem_u32(&sh.xch[turn][rank]), t), v);
-      cluster_sync();
-    } else {
-      if (t == 0) sh.xch[turn][0] = v;
-      __syncthreads();
-    }
-    return sh.xch[turn];
-  };
   auto sync_all = [&]() {
     if (cs > 1) cluster_sync();
     else __syncthreads();
   };
-  auto warp_sum64 = [&](unsigned long long v) {
+  // Three values (the same in every thread) of this rank to all ranks; returns the sums over all ranks in v and over the
+  // ranks before this one in pre.  Two buffers in turn.
+  int turn = 0;
+  auto exchange = [&](unsigned long long* v, unsigned long long* pre) {
+    turn ^= 1;
+    for (int x = t; x < 3 * cs; x += kSampleThreads)
+      st_dsmem_u64(mapa_shared(smem_u32(&sh.xch[turn][rank][x % 3]), x / 3), x % 3 == 0 ? v[0] : x % 3 == 1 ? v[1] : v[2]);
+    sync_all();
+    v[0] = v[1] = v[2] = pre[0] = pre[1] = pre[2] = 0;
+    for (int r = 0; r < cs; ++r)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
+      for (int e = 0; e < 3; ++e) {
+        if (r < rank) pre[e] += sh.xch[turn][r][e];
+        v[e] += sh.xch[turn][r][e];
+      }
   };
   // sum over the CTA's threads, and the sum over the threads before this one
   auto block_scan = [&](unsigned long long v, unsigned long long* before) {
-    unsigned long long c = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, c, o);
-      if (lane >= o) c += y;
-    }
+    const unsigned long long c = warp_scan(v, lane);
     __syncthreads();
     if (lane == 31) sh.red[warp] = c;
     __syncthreads();
-    unsigned long long pre = 0, all = 0;
-#pragma unroll 1
-    for (int w = 0; w < W; ++w) {
-      if (w < warp) pre += sh.red[w];
-      all += sh.red[w];
-    }
-    *before = pre + c - v;
-    return all;
+    const unsigned long long all = warp_scan(sh.red[lane], lane), pre = __shfl_sync(0xFFFFFFFFu, all, max(warp, 1) - 1);
+    *before = (warp ? pre : 0) + c - v;
+    return __shfl_sync(0xFFFFFFFFu, all, 31);
   };
 
   // ------------------------------------------------------------------ the slice, and the largest logit (lowest id first)
   unsigned long long best = 0;
   auto look = [&](float x, int i) {
     const uint32_t k = logit_key(x);
-    if (k) {
-      const unsigned long long v = (static_cast<unsigned long long>(k) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id0 + i));
-      best = v > best ? v : best;
-    }
+    const unsigned long long v = (static_cast<unsigned long long>(k) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id0 + i));
+    best = k && v > best ? v : best;
   };
   {
     // 16-byte loads from the first aligned address on; xs shifted alike
@@ -277,7 +294,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_logits_kernel(const 
         }
       }
     }
-    for (int i = t; i < 32 * 32; i += kSampleThreads) sh.tab[i] = kPow32[i >> 5];
+    sh.tab[t] = kPow32[t >> 5];
     if (t == kSampleThreads - 1) {
       const double c = temperature_scale(T);
       sh.scale[0] = static_cast<float>(c);
@@ -298,11 +315,17 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_logits_kernel(const 
   }
   if (lane == 0) sh.red[warp] = best;
   __syncthreads();
-  for (int w = 0; w < W; ++w) best = sh.red[w] > best ? sh.red[w] : best;
-  if (cs > 1) cluster_wait();
-  {
-    const unsigned long long* all = exchange(best);
-    for (int r = 0; r < cs; ++r) best = all[r] > best ? all[r] : best;
+  best = sh.red[lane];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const unsigned long long y = __shfl_xor_sync(0xFFFFFFFFu, best, o);
+    best = y > best ? y : best;
+  }
+  if (cs > 1) {
+    cluster_wait();
+    unsigned long long v[3] = {best, 0, 0}, pre[3];
+    exchange(v, pre);
+    for (int r = 0; r < cs; ++r) best = sh.xch[turn][r][0] > best ? sh.xch[turn][r][0] : best;
   }
   if (best == 0 || !(T > 0.0f)) {  // the whole cluster alike
     if (rank == 0 && t == 0) {
@@ -320,244 +343,248 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_logits_kernel(const 
   const float mx = key_logit(max_key);
   const RowWeights rw =
       row_weights(mx, sh.scale[0], sh.scale[1], needs_shift(mx, sh.scale[0]) ? mx : 0.0f, 1600.0f / sh.scale[0]);
-
   const int top_k = a.top_k ? a.top_k[row] : 0;
   const float top_p = a.top_p ? a.top_p[row] : 1.0f, min_p = a.min_p ? a.min_p[row] : 0.0f;
-  const bool cut_k = top_k > 0 && top_k < a.vocab, cut_p = top_p < 1.0f;
-  const unsigned long long w_max = row_weight(rw, mx, tab);
-  const unsigned long long floor_w = max(1ull, share_of(w_max, min_p));
+  bool cut_k = top_k > 0 && top_k < a.vocab, cut_p = top_p < 1.0f;
+  const unsigned long long floor_w = max(1ull, share_of(row_weight(rw, mx, tab), min_p));
+  // kept: key > thr, and the first `ties` ids of key == thr, of which there are `equals`
+  uint32_t thr = 0;
+  int ties = 0, equals = 0;
 
-  // ------------------------------------------------------------------ the tokens that can be kept, gathered where they are few
+  // ------------------------------------------------------------------ the tokens that decide, gathered where they are few
   if (cut_k || cut_p) {
-    // bins of 1/64 below the maximum; the last holds all the rest
-    auto bin_of = [&](float x) { return min(kSampleBins - 1, static_cast<int>((mx - fmaxf(x, -3.0e38f)) * 64.0f)); };
-    uint32_t* count = reinterpret_cast<uint32_t*>(sh.mass);
-    for (int i = t; i < kSampleBins; i += kSampleThreads) count[i] = 0;
+    // bins of equal widths below the maximum, the last for all the rest: for counts of 1/64, for masses of 1/51.2 octave, so
+    // that 40 octaves are covered
+    const float per_unit = cut_k ? 64.0f : 1.6f * rw.ch;
+    auto place = [&](float x) { return fminf((mx - fmaxf(x, -3.0e38f)) * per_unit, static_cast<float>(kSampleBins - 1)); };
+    for (int i = t; i < 4 * kSampleBins; i += kSampleThreads) sh.hist[0][i] = 0;
     __syncthreads();
-    unsigned long long sum = 0, before;
-#pragma unroll 1
+    unsigned long long before;
+#pragma unroll 4
     for (int i = t; i < n; i += kSampleThreads) {
       const float x = xs[i];
-      const int b = bin_of(x);
-      if (b < kSampleBins - 1) atomicAdd(&count[b], 1u);
-      if (!cut_k && logit_key(x)) sum += row_weight(rw, x, tab);
+      const int b = static_cast<int>(place(x));
+      if (cut_k) {
+        if (b < kSampleBins - 1) atomicAdd(&sh.hist[3][b], 1u);
+      } else if (x > -INFINITY) {  // (also not NaN)
+        atomicAdd(&sh.hist[3][b], 1u);
+        add_mass(sh.hist, b, row_weight(rw, x, tab));
+      }
     }
-    // the goal: k tokens, or p of the row's mass, which tokens of the first bins reach even at their bins' lowest weights
-    unsigned long long goal = static_cast<unsigned long long>(top_k);
-    if (!cut_k) {
-      const unsigned long long own = block_scan(sum, &before);
-      const unsigned long long* all = exchange(own);  // every rank's counts are there, too
-      unsigned long long total = 0;
-      for (int r = 0; r < cs; ++r) total += all[r];
-      goal = max(1ull, share_of(total, top_p));
-    } else {
-      sync_all();
-    }
+    sync_all();
     const int mine = kSampleBins / cs, each = max(1, mine / kSampleThreads), b0 = rank * mine + t * each;
-    const float wm = ex2((rw.ch * (mx - rw.sh) - rw.mo) * (1.0f / 32.0f)) * (0.999f * 0x1p44f);
-    auto value = [&](int b) -> unsigned long long {
-      uint32_t c = 0;
-      for (int r = 0; r < cs; ++r) c += __float_as_uint(ld_dsmem_f32(mapa_shared(smem_u32(&count[b]), r)));
-      if (cut_k) return c;
-      const float w = wm * ex2(static_cast<float>(b + 1) * rw.ch * (-1.0f / 2048.0f));
-      return b == 0 ? __float2ull_rd(static_cast<float>(c - 1) * w + wm) : __float2ull_rd(static_cast<float>(c) * w);
-    };
-    sum = 0;
-    if (t * each < mine)
-      for (int e = 0; e < each; ++e) sum += value(b0 + e);
-    const unsigned long long own = block_scan(sum, &before);
-    const unsigned long long* all = exchange(own);
-    unsigned long long total = 0;
-    for (int r = 0; r < cs; ++r) {
-      if (r < rank) before += all[r];
-      total += all[r];
-    }
-    if (total >= goal) {  // the cluster alike: the goal is reached before the last bin
-      if (before < goal && goal <= before + sum) {  // one thread of the cluster
-        int e = 0;
-        for (; e < each - 1; ++e) {
-          before += value(b0 + e);
-          if (goal <= before) break;
+    unsigned long long val[2], cnt[2], val_s = 0, cnt_s = 0, cnt_b;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      val[e] = cnt[e] = 0;
+      if (e < each && t * each < mine)
+        for (int r = 0; r < cs; ++r) {
+          cnt[e] += ld_dsmem_u32(mapa_shared(smem_u32(&sh.hist[3][b0 + e]), r));
+          if (!cut_k)
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+              val[e] += static_cast<unsigned long long>(ld_dsmem_u32(mapa_shared(smem_u32(&sh.hist[p][b0 + e]), r))) << (16 * p);
         }
-        for (int r = 0; r < cs; ++r) st_dsmem_u64(mapa_shared(smem_u32(&sh.found[0]), r), static_cast<unsigned long long>(b0 + e));
+      if (cut_k) val[e] = cnt[e];
+      val_s += val[e];
+      cnt_s += cnt[e];
+    }
+    unsigned long long v[3], pre[3];
+    v[0] = block_scan(val_s, &before);
+    v[1] = block_scan(cnt_s, &cnt_b);
+    v[2] = 0;
+    exchange(v, pre);
+    before += pre[0];
+    cnt_b += pre[1];
+    // the goal: k tokens, or p of the row's mass
+    unsigned long long goal = cut_k ? static_cast<unsigned long long>(top_k) : max(1ull, share_of(v[0], top_p));
+    if (v[0] >= goal) {  // the cluster alike (else there are fewer tokens than k, or the last bin hides the k-th)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (before < goal && goal <= before + val[e])  // one thread of the cluster
+          for (int r = 0; r < cs; ++r) {
+            st_dsmem_u64(mapa_shared(smem_u32(&sh.found[0]), r), static_cast<unsigned long long>(b0 + e));
+            st_dsmem_u64(mapa_shared(smem_u32(&sh.found[1]), r), cnt_b + cnt[e]);
+            st_dsmem_u64(mapa_shared(smem_u32(&sh.found[2]), r), cnt[e]);
+            st_dsmem_u64(mapa_shared(smem_u32(&sh.found[3]), r), goal - before);
+          }
+        before += val[e];
+        cnt_b += cnt[e];
       }
       sync_all();
-      const int border = static_cast<int>(sh.found[0]);
-      // this thread's run of ids (an odd number of them: no bank conflicts), its candidates and their place
-      const int len = ((n + kSampleThreads - 1) / kSampleThreads) | 1, i0 = min(n, t * len), i1 = min(n, i0 + len);
-      int cand = 0;
-      for (int i = i0; i < i1; ++i) cand += bin_of(xs[i]) <= border;
-      unsigned long long at;
-      const unsigned long long mine_c = block_scan(static_cast<unsigned long long>(cand), &at);
-      const unsigned long long* every = exchange(mine_c);
-      unsigned long long cands = 0;
-      for (int r = 0; r < cs; ++r) {
-        if (r < rank) at += every[r];
-        cands += every[r];
-      }
-      if (cands <= kSampleList) {
-        // an entry is larger the earlier its token comes in falling order
-        const uint32_t list_u = mapa_shared(smem_u32(&sh.mass[kSampleBins - kSampleList]), 0);
-        if (cand)
-          for (int i = i0; i < i1; ++i)
-            if (bin_of(xs[i]) <= border)
-              st_dsmem_u64(list_u + 8 * static_cast<uint32_t>(at++),
-                           (static_cast<unsigned long long>(logit_key(xs[i])) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id0 + i)));
-        sync_all();
-        if (rank != 0) return;
-        // ---------------------------------------------------------------- one CTA finishes the row: two entries a thread
-        const unsigned long long* list = &sh.mass[kSampleBins - kSampleList];
-        unsigned long long* hist = sh.mass;                                   // [kSampleList] bins
-        unsigned long long* vals = reinterpret_cast<unsigned long long*>(sample_smem + sizeof(SampleShared));  // [kSampleList]
-        const int N = static_cast<int>(cands);
-        unsigned long long ent[2], w[2];
-        int bin[2];
-        bool keep[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int j = 2 * t + e;
-          keep[e] = j < N;
-          ent[e] = keep[e] ? list[j] : 0;
-          const float x = key_logit(static_cast<uint32_t>(ent[e] >> 32));
-          w[e] = keep[e] ? row_weight(rw, x, tab) : 0;
-          bin[e] = keep[e] ? bin_of(x) / (kSampleBins / kSampleList) : kSampleList - 1;
-        }
-        // keeps the entries before which (in falling order) less than the goal has been kept: of tokens, or of mass
-#pragma unroll 1
-        for (int step = cut_k ? 0 : 1; step < (cut_p ? 2 : 1); ++step) {
-          const bool by_mass = step == 1;
-          unsigned long long v[2], pre;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) v[e] = !keep[e] ? 0 : by_mass ? w[e] : 1;
-          if (by_mass && cut_k) goal = max(1ull, share_of(block_scan(v[0] + v[1], &pre), top_p));
-          __syncthreads();
-          hist[2 * t] = hist[2 * t + 1] = 0;
-          __syncthreads();
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (v[e]) atomicAdd(&hist[bin[e]], v[e]);
-          __syncthreads();
-          const unsigned long long h0 = hist[2 * t], h1 = hist[2 * t + 1];
-          const unsigned long long in_all = block_scan(h0 + h1, &pre);
-          if (in_all > goal || by_mass) {  // (else every entry stays)
-            if (pre < goal && goal <= pre + h0 + h1) {
-              const bool first = goal <= pre + h0;
-              sh.found[0] = 2 * t + (first ? 0 : 1);
-              sh.found[1] = goal - (first ? pre : pre + h0);
-            }
-            __syncthreads();
-            const int border2 = static_cast<int>(sh.found[0]);
-            const unsigned long long rest = sh.found[1];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) vals[2 * t + e] = bin[e] == border2 ? v[e] : 0;
-            __syncthreads();
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              if (!keep[e]) continue;
-              if (bin[e] == border2) {
-                unsigned long long better = 0;
-                for (int j = 0; j < N; ++j) better += list[j] > ent[e] ? vals[j] : 0;
-                keep[e] = better < rest;
-              } else {
-                keep[e] = bin[e] < border2;
-              }
-            }
+      const int last = static_cast<int>(sh.found[0]);  // the bin in which the goal is reached
+      const bool complete = sh.found[1] <= kSampleList;  // every token that can be kept fits; else the border bin's tokens may
+      const int first = complete ? 0 : last;
+      if (complete || sh.found[2] <= kSampleList) {
+        if (!complete) goal = sh.found[3];
+#pragma unroll 4
+        for (int i0 = 0; i0 < n; i0 += kSampleThreads) {
+          const int i = i0 + t;
+          const float x = i < n ? xs[i] : -INFINITY;
+          const int b = static_cast<int>(place(x));
+          const bool in = b >= first && b <= last && x > -INFINITY;
+          const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
+          if (who) {
+            uint32_t at = 0;
+            if (lane == __ffs(who) - 1) at = atom_add_dsmem(mapa_shared(smem_u32(&sh.n_list), 0), __popc(who));
+            at = __shfl_sync(0xFFFFFFFFu, at, __ffs(who) - 1) + __popc(who & ((1u << lane) - 1));
+            if (in && at < kSampleList)
+              st_dsmem_u64(mapa_shared(smem_u32(&sh.list[at]), 0),
+                           (static_cast<unsigned long long>(logit_key(x)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id0 + i)));
           }
         }
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (!keep[e] || w[e] < floor_w) w[e] = 0;
-        unsigned long long run;
-        const unsigned long long total_w = block_scan(w[0] + w[1], &run);
-        const unsigned long long want = max(1ull, share_of(total_w, a.u[row]));
-        if (run < want && want <= run + w[0] + w[1]) {
-          const int e = want <= run + w[0] ? 0 : 1;
-          a.tokens[row] = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(ent[e]));
-          if (a.logprob) a.logprob[row] = log_share(rw, key_logit(static_cast<uint32_t>(ent[e] >> 32)), T, total_w);
+        sync_all();
+        if (complete && rank != 0) return;
+        if (rank == 0) {
+          // -------------------------------------------------------------- one CTA has the list: an entry a thread
+          const int N = min(static_cast<int>(sh.n_list), kSampleList);
+          const unsigned long long ent = t < N ? sh.list[t] : 0;
+          const float x = key_logit(static_cast<uint32_t>(ent >> 32));
+          const unsigned long long w = t < N ? row_weight(rw, x, tab) : 0;
+          const float fine = static_cast<float>(kSampleList) / static_cast<float>(last - first + 1);
+          const int bin = t < N ? max(0, min(kSampleList - 1, static_cast<int>((place(x) - static_cast<float>(first)) * fine))) : kSampleList - 1;
+          bool keep = t < N;
+          // Where the values v, in the order of falling `ord` (bins ascending), reach the goal: the border bin; an entry in it
+          // gets what comes before it there, and the bin's part of the goal.
+          auto reach = [&](unsigned long long ord, int b, unsigned long long val, unsigned long long to, int* border,
+                           unsigned long long* ahead, unsigned long long* rest) {
+            sh.hist[0][t] = sh.hist[1][t] = sh.hist[2][t] = 0;
+            if (t == 0) sh.members = 0;
+            __syncthreads();
+            if (val) add_mass(sh.hist, b, val);
+            __syncthreads();
+            unsigned long long p;
+            const unsigned long long h = sh.hist[0][t] + (static_cast<unsigned long long>(sh.hist[1][t]) << 16) +
+                                         (static_cast<unsigned long long>(sh.hist[2][t]) << 32);
+            block_scan(h, &p);
+            if (p < to && to <= p + h) {
+              sh.found[0] = static_cast<unsigned long long>(t);
+              sh.found[1] = to - p;
+            }
+            __syncthreads();
+            *border = static_cast<int>(sh.found[0]);
+            *rest = sh.found[1];
+            *ahead = 0;
+            if (b == *border && val) {
+              const uint32_t at = atomicAdd(&sh.members, 1u);
+              sh.ord[at] = ord;
+              sh.vals[at] = val;
+            }
+            __syncthreads();
+            if (b == *border && val) {
+              const int m = static_cast<int>(sh.members);
+              for (int j = 0; j < m; ++j) *ahead += sh.ord[j] > ord ? sh.vals[j] : 0;
+            }
+            __syncthreads();
+          };
+          int border;
+          unsigned long long ahead, rest;
+#pragma unroll 1
+          for (int step = cut_k ? 0 : 1; step < (cut_p && (complete || !cut_k) ? 2 : 1); ++step) {
+            const unsigned long long val = keep ? (step ? w : 1) : 0;
+            if (step && cut_k) goal = max(1ull, share_of(block_scan(val, &before), top_p));
+            if (!step && goal >= static_cast<unsigned long long>(N)) continue;  // all stay
+            reach(ent, bin, val, goal, &border, &ahead, &rest);
+            keep = keep && (bin < border || (bin == border && val && ahead < rest));
+          }
+          if (complete) {
+            const unsigned long long kw = keep && w >= floor_w ? w : 0;
+            const unsigned long long total = block_scan(kw, &before);
+            const uint32_t low = static_cast<uint32_t>(ent);  // ~id: larger = lower id
+            const int id = static_cast<int>(0xFFFFFFFFu - low);
+            reach(low, t < N ? min(kSampleList - 1, static_cast<int>(static_cast<float>(id) * (static_cast<float>(kSampleList) / a.vocab))) : 0, kw,
+                  max(1ull, share_of(total, a.u[row])), &border, &ahead, &rest);
+            if (kw && ahead < rest && rest <= ahead + kw &&
+                border == min(kSampleList - 1, static_cast<int>(static_cast<float>(id) * (static_cast<float>(kSampleList) / a.vocab)))) {
+              a.tokens[row] = id;
+              if (a.logprob) a.logprob[row] = log_share(rw, x, T, total);
+            }
+            return;
+          }
+          // the smallest kept key and its numbers, for everybody
+          uint32_t k = keep ? static_cast<uint32_t>(ent >> 32) : 0xFFFFFFFFu;
+          k = __reduce_min_sync(0xFFFFFFFFu, k);
+          if (lane == 0) sh.red[warp] = k;
+          __syncthreads();
+          k = __reduce_min_sync(0xFFFFFFFFu, static_cast<uint32_t>(sh.red[lane]));
+          const bool eq = t < N && static_cast<uint32_t>(ent >> 32) == k;
+          const int kept_eq = __syncthreads_count(eq && keep), all_eq = __syncthreads_count(eq);
+          if (t < 3 * cs)
+            st_dsmem_u64(mapa_shared(smem_u32(&sh.found[t % 3]), t / 3), t % 3 == 0 ? k : static_cast<unsigned long long>(t % 3 == 1 ? kept_eq : all_eq));
         }
-        return;
+        sync_all();
+        thr = static_cast<uint32_t>(sh.found[0]);
+        ties = static_cast<int>(sh.found[1]);
+        equals = static_cast<int>(sh.found[2]);
+        if (!cut_k) cut_p = false;  // done
+        cut_k = false;
+        sync_all();
       }
     }
   }
 
-  // ------------------------------------------------------------------ thresholds
-  // kept: key > thr, and the first `ties` ids of key == thr
-  uint32_t thr = 0;
-  int ties = 0, equals = 0;  // equals: how many tokens have that key
+  // ------------------------------------------------------------------ thresholds by the key's digits, over the cluster
   // Finds the key at which a sum over tokens in falling order reaches a goal: tokens counted (goal = k), or their mass
-  // (goal = p of the mass of those kept so far).
+  // (goal = share of the mass of those kept so far).
   auto select = [&](bool by_mass, float share, unsigned long long goal) {
     uint32_t prefix = 0;
     const unsigned long long w_thr = by_mass && thr ? row_weight(rw, key_logit(thr), tab) : 0;
 #pragma unroll 1
     for (int level = 0; level < 3; ++level) {
       const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11, bins = 1 << bits;
-      for (int i = t; i < bins; i += kSampleThreads) sh.mass[i] = 0;
+      for (int i = t; i < bins; i += kSampleThreads) sh.hist[0][i] = sh.hist[1][i] = sh.hist[2][i] = 0;
       __syncthreads();
-      uint32_t* count = reinterpret_cast<uint32_t*>(sh.mass);
-#pragma unroll 1
+#pragma unroll 2
       for (int i = t; i < n; i += kSampleThreads) {
         const float x = xs[i];
         const uint32_t k = logit_key(x);
-        if (k == 0 || (level && (k >> (shift + bits)) != (prefix >> (shift + bits)))) continue;
+        if (k == 0 || (level && (k >> (shift + bits)) != (prefix >> (shift + bits))) || (by_mass && k <= thr)) continue;
         const int bin = bins - 1 - ((k >> shift) & (bins - 1));  // largest first
-        if (!by_mass) atomicAdd(&count[bin], 1u);
-        else if (k > thr) atomicAdd(&sh.mass[bin], row_weight(rw, x, tab));
+        if (by_mass) add_mass(sh.hist, bin, row_weight(rw, x, tab));
+        else atomicAdd(&sh.hist[0][bin], 1u);
       }
-      if (by_mass && rank == 0 && t == 0 && thr && (!level || (thr >> (shift + bits)) == (prefix >> (shift + bits))))
-        atomicAdd(&sh.mass[bins - 1 - ((thr >> shift) & (bins - 1))], w_thr * static_cast<unsigned long long>(ties));
       sync_all();
       // this rank's share of the bins, over all ranks
       const int mine = bins / cs, each = max(1, mine / kSampleThreads), b0 = rank * mine + t * each;
-      unsigned long long sum = 0, before;
-      if (t * each < mine)
-        for (int e = 0; e < each; ++e)
+      unsigned long long val[2], sum = 0, before, pre[3];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        val[e] = 0;
+        if (e < each && t * each < mine)
           for (int r = 0; r < cs; ++r)
-            sum += by_mass ? ld_dsmem_u64(mapa_shared(smem_u32(&sh.mass[b0 + e]), r))
-                           : __float_as_uint(ld_dsmem_f32(mapa_shared(smem_u32(&count[b0 + e]), r)));
-      const unsigned long long own = block_scan(sum, &before);
-      const unsigned long long* all = exchange(own);
-      unsigned long long total = 0;
-      for (int r = 0; r < cs; ++r) {
-        if (r < rank) before += all[r];
-        total += all[r];
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+              val[e] += static_cast<unsigned long long>(ld_dsmem_u32(mapa_shared(smem_u32(&sh.hist[p][b0 + e]), r))) << (16 * p);
+        // the equals of an earlier threshold, as many as stay
+        if (by_mass && thr && e < each && t * each < mine && (!level || (thr >> (shift + bits)) == (prefix >> (shift + bits))) &&
+            b0 + e == bins - 1 - static_cast<int>((thr >> shift) & (bins - 1)))
+          val[e] += w_thr * static_cast<unsigned long long>(ties);
+        sum += val[e];
       }
+      unsigned long long v[3] = {block_scan(sum, &before), 0, 0};
+      exchange(v, pre);
+      before += pre[0];
       if (level == 0) {
-        if (by_mass) goal = max(1ull, share_of(total, share));
-        else if (goal >= total) return;  // no more tokens than that: nothing to cut
+        if (by_mass) goal = max(1ull, share_of(v[0], share));
+        else if (goal >= v[0]) return;  // no more tokens than that: nothing to cut
       }
-      if (before < goal && goal <= before + sum) {  // one thread of the cluster
-        unsigned long long v = 0;
-        int e = 0;
-        for (;; ++e) {
-          v = 0;
-          for (int r = 0; r < cs; ++r)
-            v += by_mass ? ld_dsmem_u64(mapa_shared(smem_u32(&sh.mass[b0 + e]), r))
-                         : __float_as_uint(ld_dsmem_f32(mapa_shared(smem_u32(&count[b0 + e]), r)));
-          if (e == each - 1 || goal <= before + v) break;
-          before += v;
-        }
-        for (int r = 0; r < cs; ++r) {
-          st_dsmem_u64(mapa_shared(smem_u32(&sh.found[0]), r), static_cast<unsigned long long>(b0 + e));
-          st_dsmem_u64(mapa_shared(smem_u32(&sh.found[1]), r), goal - before);
-          st_dsmem_u64(mapa_shared(smem_u32(&sh.found[2]), r), v);
-        }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (before < goal && goal <= before + val[e])  // one thread of the cluster
+          for (int r = 0; r < cs; ++r) {
+            st_dsmem_u64(mapa_shared(smem_u32(&sh.found[0]), r), static_cast<unsigned long long>(b0 + e));
+            st_dsmem_u64(mapa_shared(smem_u32(&sh.found[1]), r), goal - before);
+            st_dsmem_u64(mapa_shared(smem_u32(&sh.found[2]), r), val[e]);
+          }
+        before += val[e];
       }
       sync_all();
       prefix |= static_cast<uint32_t>(bins - 1 - static_cast<int>(sh.found[0])) << shift;
       goal = sh.found[1];
     }
     // of the border's equals, as many as the rest of the goal needs
-    const unsigned long long v = sh.found[2];
-    int need, have;
-    if (by_mass) {
-      const unsigned long long w = row_weight(rw, key_logit(prefix), tab);
-      need = static_cast<int>((goal + w - 1) / w);
-      have = static_cast<int>(v / w);
-    } else {
-      need = static_cast<int>(goal);
-      have = static_cast<int>(v);
-    }
+    const unsigned long long v = sh.found[2], w = by_mass ? row_weight(rw, key_logit(prefix), tab) : 1;
+    const int need = static_cast<int>((goal + w - 1) / w), have = static_cast<int>(v / w);
     if (prefix != thr) {
       thr = prefix;
       ties = need;
@@ -565,109 +592,70 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_logits_kernel(const 
     } else {
       ties = min(ties, need);
     }
+    sync_all();  // everybody has read what was found
   };
   if (cut_k) select(false, 0.0f, static_cast<unsigned long long>(top_k));
   if (cut_p) select(true, top_p, 0);
   const unsigned long long w_thr0 = thr ? row_weight(rw, key_logit(thr), tab) : 0, w_thr = w_thr0 >= floor_w ? w_thr0 : 0;
+  const bool all_ties = ties >= equals;  // every equal of the threshold stays (or there is none)
   // weight of token i of the slice; ties are left to the caller
   auto kept_weight = [&](int i, bool* tie) -> unsigned long long {
     const float x = xs[i];
     const uint32_t k = logit_key(x);
     *tie = k && k == thr;
-    if (k <= thr) return 0;
-    const unsigned long long w = row_weight(rw, x, tab);
+    const unsigned long long w = k > thr ? row_weight(rw, x, tab) : 0;
     return w >= floor_w ? w : 0;
   };
-  const bool all_ties = ties >= equals;  // every equal of the threshold stays (or there is none)
-
-  // ------------------------------------------------------------------ total, and the part of the row that holds the goal
-  // Three rounds: the cluster's slices, a warp's part of a slice, a thread's part of that.
-  const int part = (n + W - 1) / W, p0 = min(n, warp * part), p1 = min(n, p0 + part);
-  unsigned long long sum = 0;
-  int eq = 0;
-#pragma unroll 1
-  for (int i = p0 + lane; i < p1; i += 32) {
-    bool tie;
-    sum += kept_weight(i, &tie);
-    eq += tie;
-  }
-  eq = __reduce_add_sync(0xFFFFFFFFu, eq);
-  sum = warp_sum64(sum);
-  __syncthreads();
-  if (lane == 0) {
-    sh.mass[warp] = sum;
-    sh.mass[W + warp] = static_cast<unsigned long long>(eq);
-  }
-  __syncthreads();
-  unsigned long long cta_sum = 0, cta_eq = 0;
-  for (int w = 0; w < W; ++w) {
-    cta_sum += sh.mass[w];
-    cta_eq += sh.mass[W + w];
-  }
-  // equals before this rank decide how many of its own stay
-  long long eq_before = 0;
-  if (!all_ties) {
-    const unsigned long long* all = exchange(cta_eq);
-    for (int r = 0; r < rank; ++r) eq_before += static_cast<long long>(all[r]);
-  }
-  auto stay = [&](long long seen, unsigned long long here) -> unsigned long long {  // equals that stay, of `here` after `seen`
+  auto stay = [&](unsigned long long seen, unsigned long long here) -> unsigned long long {  // equals that stay, of `here` after `seen`
     if (all_ties) return here;
-    const long long room = static_cast<long long>(ties) - seen;
-    return room <= 0 ? 0 : min(here, static_cast<unsigned long long>(room));
+    return seen >= static_cast<unsigned long long>(ties) ? 0 : min(here, static_cast<unsigned long long>(ties) - seen);
   };
-  cta_sum += w_thr * stay(eq_before, cta_eq);
-  unsigned long long run = 0, total = 0;
-  {
-    const unsigned long long* all = exchange(cta_sum);
-    for (int r = 0; r < cs; ++r) {
-      if (r < rank) run += all[r];
-      total += all[r];
-    }
-  }
-  const unsigned long long goal = max(1ull, share_of(total, a.u[row]));
-  if (!(run < goal && goal <= run + cta_sum)) return;  // another CTA's (no rank looks into another's memory from here on)
-  int q0 = 0, q1 = n;
-  long long seen = eq_before;
-#pragma unroll 1
-  for (int w = 0; w < W; ++w) {
-    const unsigned long long m = sh.mass[w] + w_thr * stay(seen, sh.mass[W + w]);
-    if (goal <= run + m) {
-      q0 = min(n, w * part);
-      q1 = min(n, q0 + part);
-      break;
-    }
-    run += m;
-    seen += static_cast<long long>(sh.mass[W + w]);
-  }
-  const int each = (q1 - q0 + kSampleThreads - 1) / kSampleThreads, r0 = min(q1, q0 + t * each), r1 = min(q1, r0 + each);
-  unsigned long long mine = 0, before;
-  int my_eq = 0;
-  for (int i = r0; i < r1; ++i) {
+
+  // ------------------------------------------------------------------ total, and the token at the goal
+  // a run of ids per thread (an odd number of them: no bank conflicts)
+  const int len = ((n + kSampleThreads - 1) / kSampleThreads) | 1, i0 = min(n, t * len), i1 = min(n, i0 + len);
+  unsigned long long mine = 0, before, seen = 0;
+  unsigned int eq = 0;
+#pragma unroll 4
+  for (int i = i0; i < i1; ++i) {
     bool tie;
     mine += kept_weight(i, &tie);
-    my_eq += tie;
+    eq += tie;
   }
-  unsigned long long eq_pre;
-  block_scan(static_cast<unsigned long long>(my_eq), &eq_pre);
-  seen += static_cast<long long>(eq_pre);
-  mine += w_thr * stay(seen, static_cast<unsigned long long>(my_eq));
-  block_scan(mine, &before);
-  run += before;
-  if (run < goal && goal <= run + mine) {
-    for (int i = r0; i < r1; ++i) {
-      bool tie;
-      unsigned long long w = kept_weight(i, &tie);
-      if (tie) {
-        w = w_thr * stay(seen, 1);
-        ++seen;
-      }
-      run += w;
-      if (w > 0 && goal <= run) {
+  unsigned long long v[3] = {0, 0, 0}, pre[3];
+  if (!all_ties) {
+    v[0] = block_scan(eq, &seen);
+    exchange(v, pre);
+    seen += pre[0];
+  }
+  mine += w_thr * stay(seen, eq);
+  v[0] = block_scan(mine, &before);
+  exchange(v, pre);
+  before += pre[0];
+  const unsigned long long total = v[0], goal = max(1ull, share_of(total, a.u[row]));
+  const uint32_t hit = __ballot_sync(0xFFFFFFFFu, before < goal && goal <= before + mine);
+  if (!hit) return;  // another warp's (no rank looks into another's memory from here on)
+  const int who = __ffs(hit) - 1, end = __shfl_sync(0xFFFFFFFFu, i1, who);
+  unsigned long long run = __shfl_sync(0xFFFFFFFFu, before, who);
+  seen = __shfl_sync(0xFFFFFFFFu, seen, who);
+#pragma unroll 1
+  for (int base = __shfl_sync(0xFFFFFFFFu, i0, who); base < end; base += 32) {
+    const int i = base + lane;
+    bool tie = false;
+    unsigned long long w = i < end ? kept_weight(i, &tie) : 0;
+    const uint32_t tb = __ballot_sync(0xFFFFFFFFu, tie);
+    if (tie) w = w_thr * stay(seen + __popc(tb & ((1u << lane) - 1)), 1);
+    seen += __popc(tb);
+    const unsigned long long c = run + warp_scan(w, lane);
+    const uint32_t got = __ballot_sync(0xFFFFFFFFu, w > 0 && goal <= c);
+    if (got) {
+      if (lane == __ffs(got) - 1) {
         a.tokens[row] = id0 + i;
         if (a.logprob) a.logprob[row] = log_share(rw, xs[i], T, total);
-        break;
       }
+      break;
     }
+    run = __shfl_sync(0xFFFFFFFFu, c, 31);
   }
 }
 

@@ -57,12 +57,13 @@ vsd_status launch_sample(SampleRowArgs& a, cudaStream_t st) {
     CK(launch_ex_cluster(sample_plain_kernel, dim3(static_cast<unsigned>(a.rows) * a.cs), dim3(kPlainThreads), 0, a.cs, st, false, a));
     return VSD_OK;
   }
+  // CTAs per row: as many as hold its slices, then more while every row still has its SMs at once
   static const int fcs = getenv("SP_CS") ? atoi(getenv("SP_CS")) : 0;
-  // CTAs per row: enough for two per SM, and slices that leave room for two (their number, where the row is long)
-  while (a.cs < kSampleMaxCluster && (a.vocab > a.cs * 18000 || (static_cast<int64_t>(a.rows) * a.cs < 2 * sms && a.vocab > a.cs * 1024))) a.cs *= 2;
+  while (a.cs < kSampleMaxCluster && (a.vocab > a.cs * 40960 || (static_cast<int64_t>(a.rows) * a.cs * 2 <= sms && a.vocab > a.cs * 2048)))
+    a.cs *= 2;
   if (fcs) a.cs = fcs;
   a.per = (ceil_div_h(a.vocab, a.cs) + 3) / 4 * 4;
-  const int smem = static_cast<int>(sizeof(SampleShared)) + std::max((a.per + 4) * 4, kSampleList * 8);
+  const int smem = static_cast<int>(sizeof(SampleShared)) + (a.per + 4) * 4;
   CK(ensure_smem_opt_in(reinterpret_cast<const void*>(sample_logits_kernel), smem));
   CK(launch_ex_cluster(sample_logits_kernel, dim3(static_cast<unsigned>(a.rows) * a.cs), dim3(kSampleThreads), smem, a.cs, st, false, a));
   return VSD_OK;
