@@ -12,14 +12,10 @@
 // of summation, so weights are integers (2^-44 of a power of two above the
 // largest; 2^18 of them stay under 2^63) and every sum is exact.  Their
 // relative error has to be far below a token's share of a 150,000-token row,
-// which float32 is not: with c = 32 / (T ln 2) in two floats, x c = N + f,
-// 2^(N / 32) from a table of 32 pairs and an exponent, exp(f ln 2 / 32) by its
-// series in pairs, about 2^-37 in 45 float32 instructions (float64 runs at a
-// fiftieth of their rate here).
-//
-// Rows without filters (sample_plain_kernel) are streamed once; each tile of
-// 512 tokens leaves its sum, against a power of two of its own, and the tile
-// that holds the sampled mass is read again.
+// which float32 is not: with c = 2^B / (T ln 2) in two floats, x c = N + f,
+// 2^(N / 2^B) from a table and an exponent, exp(f ln 2 / 2^B) by its series in
+// pairs, some 40 float32 instructions (float64 runs at a fiftieth of their rate
+// here).
 //
 // With filters (sample_logits_kernel) a row's logits are read once into the
 // shared memory of a cluster of CTAs.  A histogram of their distance from the
@@ -60,49 +56,130 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
 
-// 2^(i / 32) as pairs.
-__device__ const float2 kPow32[32] = {
-    {0x1.0000000000000p+0f, 0x0.0p+0f}, {0x1.059b0e0000000p+0f, -0x1.9d4f520000000p-25f}, {0x1.0b55860000000p+0f, 0x1.9f31220000000p-25f},
-    {0x1.11301e0000000p+0f, -0x1.fdb4960000000p-25f}, {0x1.172b840000000p+0f, -0x1.c157420000000p-27f}, {0x1.1d48740000000p+0f, -0x1.d2e8ca0000000p-25f},
-    {0x1.2387a60000000p+0f, 0x1.ceac480000000p-25f}, {0x1.29e9e00000000p+0f, -0x1.5c04240000000p-25f}, {0x1.306fe00000000p+0f, 0x1.4636e20000000p-25f},
-    {0x1.371a740000000p+0f, -0x1.18aac60000000p-25f}, {0x1.3dea640000000p+0f, 0x1.8246840000000p-25f}, {0x1.44e0860000000p+0f, 0x1.8624b40000000p-30f},
-    {0x1.4bfdae0000000p+0f, -0x1.593abc0000000p-25f}, {0x1.5342b60000000p+0f, -0x1.2c56100000000p-25f}, {0x1.5ab07e0000000p+0f, -0x1.5bd5ec0000000p-27f},
-    {0x1.6247ec0000000p+0f, -0x1.f8b5500000000p-25f}, {0x1.6a09e60000000p+0f, 0x1.9fcef40000000p-26f}, {0x1.71f75e0000000p+0f, 0x1.1d8bee0000000p-25f},
-    {0x1.7a11480000000p+0f, -0x1.829fd00000000p-25f}, {0x1.82589a0000000p+0f, -0x1.accc7c0000000p-26f}, {0x1.8ace540000000p+0f, 0x1.15506e0000000p-27f},
-    {0x1.93737c0000000p+0f, -0x1.e647440000000p-25f}, {0x1.9c49180000000p+0f, 0x1.51f8480000000p-27f}, {0x1.a5503c0000000p+0f, -0x1.b83b540000000p-25f},
-    {0x1.ae89fa0000000p+0f, -0x1.a94b140000000p-26f}, {0x1.b7f7700000000p+0f, -0x1.a094380000000p-25f}, {0x1.c199be0000000p+0f, -0x1.3d56b20000000p-27f},
-    {0x1.cb720e0000000p+0f, -0x1.8837cc0000000p-27f}, {0x1.d5818e0000000p+0f, -0x1.822dbc0000000p-27f}, {0x1.dfc9740000000p+0f, -0x1.908c940000000p-25f},
-    {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}, {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f}};
+// 2^(i / 128): rounded, and the relative rest.
+__device__ const float2 kPow128[128] = {
+    {0x1.0000000000000p+0f, 0x0.0p+0f}, {0x1.0163da0000000p+0f, 0x1.3dacd20000000p-25f}, {0x1.02c9a40000000p+0f, -0x1.8445420000000p-28f},
+    {0x1.04315e0000000p+0f, 0x1.0976e40000000p-25f}, {0x1.059b0e0000000p+0f, -0x1.9474140000000p-25f}, {0x1.0706b20000000p+0f, 0x1.334fa40000000p-25f},
+    {0x1.0874520000000p+0f, -0x1.d32b6e0000000p-26f}, {0x1.09e3ec0000000p+0f, 0x1.4c0a740000000p-25f}, {0x1.0b55860000000p+0f, 0x1.8d96d40000000p-25f},
+    {0x1.0cc9220000000p+0f, 0x1.5cdc900000000p-25f}, {0x1.0e3ec40000000p+0f, -0x1.8f4da60000000p-25f}, {0x1.0fb66a0000000p+0f, 0x1.e240f40000000p-25f},
+    {0x1.11301e0000000p+0f, -0x1.dda2fc0000000p-25f}, {0x1.12abdc0000000p+0f, 0x1.935bf00000000p-30f}, {0x1.1429aa0000000p+0f, 0x1.b2e5100000000p-25f},
+    {0x1.15a98c0000000p+0f, 0x1.fe37240000000p-26f}, {0x1.172b840000000p+0f, -0x1.9c0c220000000p-27f}, {0x1.18af940000000p+0f, -0x1.b2ec180000000p-26f},
+    {0x1.1a35be0000000p+0f, 0x1.4bfc220000000p-25f}, {0x1.1bbe080000000p+0f, 0x1.cfe8860000000p-27f}, {0x1.1d48740000000p+0f, -0x1.a2fbb20000000p-25f},
+    {0x1.1ed5020000000p+0f, 0x1.5551100000000p-27f}, {0x1.2063b80000000p+0f, 0x1.dc5dea0000000p-26f}, {0x1.21f49a0000000p+0f, -0x1.99e61e0000000p-25f},
+    {0x1.2387a60000000p+0f, 0x1.9649040000000p-25f}, {0x1.251ce40000000p+0f, 0x1.b6ba560000000p-25f}, {0x1.26b4560000000p+0f, 0x1.4728b60000000p-26f},
+    {0x1.284dfe0000000p+0f, 0x1.b130060000000p-28f}, {0x1.29e9e00000000p+0f, -0x1.2b0dbc0000000p-25f}, {0x1.2b87fe0000000p+0f, -0x1.9e35be0000000p-25f},
+    {0x1.2d285a0000000p+0f, 0x1.76e0400000000p-26f}, {0x1.2ecafa0000000p+0f, 0x1.f4214e0000000p-26f}, {0x1.306fe00000000p+0f, 0x1.1250020000000p-25f},
+    {0x1.3217100000000p+0f, -0x1.8c14440000000p-27f}, {0x1.33c08c0000000p+0f, -0x1.6a41980000000p-25f}, {0x1.356c560000000p+0f, -0x1.69f6f00000000p-30f},
+    {0x1.371a740000000p+0f, -0x1.cde8ce0000000p-26f}, {0x1.38cae60000000p+0f, 0x1.5511020000000p-25f}, {0x1.3a7db40000000p+0f, -0x1.21376e0000000p-25f},
+    {0x1.3c32dc0000000p+0f, 0x1.3eda020000000p-27f}, {0x1.3dea640000000p+0f, 0x1.370be40000000p-25f}, {0x1.3fa4500000000p+0f, 0x1.df22ee0000000p-27f},
+    {0x1.4160a20000000p+0f, 0x1.90d1a40000000p-28f}, {0x1.431f5e0000000p+0f, -0x1.52f5f40000000p-26f}, {0x1.44e0860000000p+0f, 0x1.336de20000000p-30f},
+    {0x1.46a41e0000000p+0f, 0x1.48dff80000000p-25f}, {0x1.486a2c0000000p+0f, -0x1.ff1cbe0000000p-26f}, {0x1.4a32b00000000p+0f, -0x1.7808940000000p-25f},
+    {0x1.4bfdae0000000p+0f, -0x1.0a35500000000p-25f}, {0x1.4dcb2a0000000p+0f, -0x1.26ea3c0000000p-26f}, {0x1.4f9b280000000p+0f, -0x1.ca37e00000000p-26f},
+    {0x1.516daa0000000p+0f, 0x1.10e5960000000p-27f}, {0x1.5342b60000000p+0f, -0x1.c541b40000000p-26f}, {0x1.551a4c0000000p+0f, 0x1.f1e1800000000p-26f},
+    {0x1.56f4740000000p+0f, -0x1.bbeca40000000p-26f}, {0x1.58d12e0000000p+0f, -0x1.0f012a0000000p-25f}, {0x1.5ab07e0000000p+0f, -0x1.00d8ac0000000p-27f},
+    {0x1.5c92680000000p+0f, 0x1.e66c800000000p-26f}, {0x1.5e76f20000000p+0f, -0x1.e2a0800000000p-26f}, {0x1.605e1c0000000p+0f, -0x1.2fe3d60000000p-26f},
+    {0x1.6247ec0000000p+0f, -0x1.6cb2840000000p-25f}, {0x1.6434640000000p+0f, -0x1.0194c80000000p-25f}, {0x1.6623880000000p+0f, 0x1.aad5be0000000p-28f},
+    {0x1.68155e0000000p+0f, -0x1.0a30c80000000p-25f}, {0x1.6a09e60000000p+0f, 0x1.26055c0000000p-26f}, {0x1.6c01280000000p+0f, -0x1.ed07cc0000000p-26f},
+    {0x1.6dfb240000000p+0f, -0x1.42c75e0000000p-27f}, {0x1.6ff7e00000000p+0f, -0x1.297d700000000p-26f}, {0x1.71f75e0000000p+0f, 0x1.8b2bb80000000p-26f},
+    {0x1.73f9a40000000p+0f, 0x1.7cd7f60000000p-26f}, {0x1.75feb60000000p+0f, -0x1.aab7960000000p-26f}, {0x1.7806940000000p+0f, 0x1.59b5a20000000p-25f},
+    {0x1.7a11480000000p+0f, -0x1.05cb440000000p-25f}, {0x1.7c1ed00000000p+0f, 0x1.9a7ca00000000p-29f}, {0x1.7e2f340000000p+0f, -0x1.89fa7a0000000p-26f},
+    {0x1.8042760000000p+0f, -0x1.f54f8e0000000p-26f}, {0x1.82589a0000000p+0f, -0x1.1c21420000000p-26f}, {0x1.8471a40000000p+0f, 0x1.02f7660000000p-26f},
+    {0x1.868d9a0000000p+0f, -0x1.8d087c0000000p-27f}, {0x1.88ac7e0000000p+0f, -0x1.0d831a0000000p-26f}, {0x1.8ace540000000p+0f, 0x1.67a1ca0000000p-28f},
+    {0x1.8cf3220000000p+0f, -0x1.7f85920000000p-26f}, {0x1.8f1aea0000000p+0f, -0x1.1bebb20000000p-26f}, {0x1.9145b00000000p+0f, 0x1.d86ad60000000p-26f},
+    {0x1.93737c0000000p+0f, -0x1.348e560000000p-25f}, {0x1.95a44c0000000p+0f, 0x1.dbe6240000000p-26f}, {0x1.97d82a0000000p+0f, -0x1.5264320000000p-32f},
+    {0x1.9a0f180000000p+0f, -0x1.2fe03a0000000p-25f}, {0x1.9c49180000000p+0f, 0x1.a3b5e40000000p-28f}, {0x1.9e86320000000p+0f, -0x1.e335e20000000p-27f},
+    {0x1.a0c6680000000p+0f, -0x1.6c46c20000000p-27f}, {0x1.a309be0000000p+0f, 0x1.e084980000000p-26f}, {0x1.a5503c0000000p+0f, -0x1.0b7ec80000000p-25f},
+    {0x1.a799e20000000p+0f, -0x1.ef74680000000p-26f}, {0x1.a9e6b60000000p+0f, -0x1.94d3de0000000p-26f}, {0x1.ac36bc0000000p+0f, -0x1.a557820000000p-32f},
+    {0x1.ae89fa0000000p+0f, -0x1.f9c3040000000p-27f}, {0x1.b0e0720000000p+0f, 0x1.69980c0000000p-26f}, {0x1.b33a2c0000000p+0f, -0x1.2187300000000p-26f},
+    {0x1.b597280000000p+0f, 0x1.04240e0000000p-25f}, {0x1.b7f7700000000p+0f, -0x1.e4c8860000000p-26f}, {0x1.ba5b040000000p+0f, -0x1.1ca7f80000000p-25f},
+    {0x1.bcc1ea0000000p+0f, -0x1.2140f60000000p-25f}, {0x1.bf2c260000000p+0f, -0x1.30d0b40000000p-27f}, {0x1.c199be0000000p+0f, -0x1.6961b40000000p-28f},
+    {0x1.c40ab60000000p+0f, -0x1.ae99940000000p-40f}, {0x1.c67f120000000p+0f, 0x1.02861c0000000p-25f}, {0x1.c8f6da0000000p+0f, -0x1.ad47f00000000p-26f},
+    {0x1.cb720e0000000p+0f, -0x1.b5151e0000000p-28f}, {0x1.cdf0b60000000p+0f, -0x1.7927a20000000p-26f}, {0x1.d072d40000000p+0f, 0x1.61cd100000000p-26f},
+    {0x1.d2f8700000000p+0f, 0x1.1a8a980000000p-26f}, {0x1.d5818e0000000p+0f, -0x1.a5217c0000000p-28f}, {0x1.d80e320000000p+0f, -0x1.3fc1d40000000p-26f},
+    {0x1.da9e600000000p+0f, 0x1.0a3cca0000000p-27f}, {0x1.dd32200000000p+0f, -0x1.be1cbe0000000p-26f}, {0x1.dfc9740000000p+0f, -0x1.ab71320000000p-26f},
+    {0x1.e264620000000p+0f, -0x1.76fb0c0000000p-26f}, {0x1.e502ee0000000p+0f, 0x1.fdadbc0000000p-27f}, {0x1.e7a5200000000p+0f, -0x1.1bab400000000p-27f},
+    {0x1.ea4afa0000000p+0f, 0x1.61428e0000000p-28f}, {0x1.ecf4820000000p+0f, 0x1.c28f6e0000000p-26f}, {0x1.efa1be0000000p+0f, 0x1.db5db60000000p-26f},
+    {0x1.f252b40000000p+0f, -0x1.1a11980000000p-26f}, {0x1.f507660000000p+0f, -0x1.2ad5f80000000p-27f}, {0x1.f7bfda0000000p+0f, 0x1.baba240000000p-26f},
+    {0x1.fa7c180000000p+0f, 0x1.a314840000000p-29f}, {0x1.fd3c220000000p+0f, 0x1.73f0780000000p-26f}};
 
-// A row's weights.
+// A row's weights with a table of 2^B powers.
+template <int B>
 struct RowWeights {
   float sh, low;   // x' = max(x - sh, low)
-  float ch, cl;    // c = 32 / (T ln 2)
-  float mo;        // N of the power of two next to the largest weight
+  float ch, cl;    // c = 2^B / (T ln 2)
+  float mo;        // N of a power of two above the largest weight
   int n_off;       // bits of the rounding constant plus that N
 };
 constexpr float kRoundMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer
+constexpr float kStep44 = 0x1.8p-21f;       // adding it rounds to 2^-44
 
 // c, capped where 1 / T leaves float32: no two different logits share the mass at one end, all share it at the other.
+template <int B>
 __device__ __forceinline__ double temperature_scale(float T) {
-  return fmin(fmax(46.166241308446828 / static_cast<double>(T), 1e-30), 1e30);
+  return fmin(fmax((1 << B) * 1.4426950408889634 / static_cast<double>(T), 1e-30), 1e30);
 }
 
 // x c must round to an integer below 2^22; beyond that only logits within a
 // factor of two of the maximum have weight, and their difference from it is exact.
 __device__ __forceinline__ bool needs_shift(float mx, float ch) { return !(fabsf(mx) * ch < 2097152.0f); }
 
-// Weights for logits up to mx (shifted by sh); drop = 1600 / c: that far below, a weight of 2^-50 is nothing.
-__device__ __forceinline__ RowWeights row_weights(float mx, float ch, float cl, float sh, float drop) {
-  RowWeights r;
+// Weights for logits up to mx.
+template <int B>
+__device__ __forceinline__ RowWeights<B> row_weights(float mx, float ch, float cl) {
+  RowWeights<B> r;
   r.ch = ch;
   r.cl = cl;
-  r.sh = sh;
-  const float m = mx - sh;
-  r.low = fmaxf(m - drop, -3.0e38f);
-  r.mo = floorf(m * ch * (1.0f / 32.0f)) * 32.0f + 32.0f;  // weights below 1 (and a little)
+  r.sh = needs_shift(mx, ch) ? mx : 0.0f;
+  const float m = mx - r.sh;
+  r.low = fmaxf(m - (50 << B) / ch, -3.0e38f);  // a weight of 2^-50: nothing
+  r.mo = (floorf(m * ch * (1.0f / (1 << B))) + 1.0f) * (1 << B);  // weights below 1 (and a little)
   r.n_off = __float_as_int(kRoundMagic) + static_cast<int>(r.mo);
   return r;
+}
+
+// Weight of x' = max(x - sh, low) as two floats whose bits count steps of 2^-22 above 2 and of 2^-44 above kStep44.
+// tab: this lane's column of the table.  FINE: relative error 2^-36 (B = 5) or 2^-38 (B = 7); else 2^-31 at most and 2^-33 in
+// the mean (B = 7), for weights that are small beside the largest.
+template <int B, bool FINE>
+__device__ __forceinline__ void weight_parts(const RowWeights<B>& r, float x, const float2* tab, float* i1, float* i2) {
+  constexpr float kh = 0x1.62e4300000000p-1f / (1 << B), kl = -0x1.05c6100000000p-29f / (1 << B);  // ln 2 / 2^B
+  float tm, s, sl = 0.0f;
+  float2 t2;
+  if (FINE) {
+    const float uh = __fmul_rn(x, r.ch);  // not to be contracted into the sums below
+    const float ul = fmaf(x, r.cl, fmaf(x, r.ch, -uh));
+    tm = uh + kRoundMagic;
+    const float f0 = uh - (tm - kRoundMagic);
+    const float f = f0 + ul, fl = ul - (f - f0);  // ul reaches 2^-3 where x c reaches 2^21
+    t2 = tab[(__float_as_int(tm) & ((1 << B) - 1)) * 32];
+    const float zh = f * kh;
+    const float zl = fmaf(fl, kh, fmaf(f, kl, fmaf(f, kh, -zh)));
+    const float poly = B == 5 ? fmaf(zh, fmaf(zh, 1.0f / 24.0f, 1.0f / 6.0f), 0.5f) : fmaf(zh, 1.0f / 6.0f, 0.5f);
+    const float rest = fmaf(t2.y, zh, fmaf(zh * zh, poly, zl)) + t2.y;
+    s = zh + rest;
+    sl = rest - (s - zh);
+  } else {
+    tm = fmaf(x, r.ch, kRoundMagic);
+    const float f = fmaf(x, r.cl, fmaf(x, r.ch, -(tm - kRoundMagic)));
+    t2 = tab[(__float_as_int(tm) & ((1 << B) - 1)) * 32];
+    const float z = f * kh;
+    s = fmaf(z * z, fmaf(z, 1.0f / 6.0f, 0.5f), z) + t2.y;
+  }
+  // t (1 + s + sl) 2^k, rounded to its steps
+  const float t = __int_as_float(__float_as_int(t2.x) + (((__float_as_int(tm) - r.n_off) >> B) << 23));
+  const float eh = fmaf(t, s, t);
+  float el = fmaf(t, s, t - eh);
+  if (FINE) el = fmaf(t, sl, el);
+  *i1 = eh + 2.0f;
+  *i2 = ((eh - (*i1 - 2.0f)) + el) + kStep44;
+}
+// Weight of logit x, in 2^-44.
+template <int B, bool FINE = true>
+__device__ __forceinline__ unsigned long long row_weight(const RowWeights<B>& r, float x, const float2* tab) {
+  float i1, i2;
+  weight_parts<B, FINE>(r, fmaxf(x - r.sh, r.low), tab, &i1, &i2);  // NaN and -inf come out as nothing
+  return (static_cast<unsigned long long>(static_cast<unsigned int>(__float_as_int(i1) - __float_as_int(2.0f))) << 22) +
+         static_cast<long long>(__float_as_int(i2) - __float_as_int(kStep44));
 }
 
 // ceil(share * total), exactly; share in [0, 1] (NaN counts as 0).
@@ -125,40 +202,12 @@ __device__ __forceinline__ unsigned long long share_of(unsigned long long total,
   return q + (rest != 0);
 }
 
-// Weight of logit x, in 2^-44; tab: this lane's column of the table.
-__device__ __forceinline__ unsigned long long row_weight(const RowWeights& r, float x, const float2* tab) {
-  x = fmaxf(x - r.sh, r.low);  // NaN and -inf come out as nothing
-  const float uh = __fmul_rn(x, r.ch);  // not to be contracted into the sums below
-  const float ul = fmaf(x, r.cl, fmaf(x, r.ch, -uh));
-  const float tm = uh + kRoundMagic;
-  const float f0 = uh - (tm - kRoundMagic);
-  const float f = f0 + ul, fl = ul - (f - f0);  // ul reaches 2^-3 where x c reaches 2^21
-  // z = (f + fl) ln 2 / 32
-  constexpr float kh = 0x1.62e4300000000p-6f, kl = -0x1.05c6100000000p-34f;
-  const float zh = f * kh;
-  const float zl = fmaf(fl, kh, fmaf(f, kl, fmaf(f, kh, -zh)));
-  const float q = zh * zh * fmaf(zh, fmaf(zh, 1.0f / 24.0f, 1.0f / 6.0f), 0.5f);
-  const float sl = zl + q;
-  const int n = __float_as_int(tm) - r.n_off;
-  const float2 t2 = tab[(n & 31) * 32];
-  const float sc = __int_as_float(((n >> 5) + 127) << 23);
-  const float ph = t2.x * zh;
-  const float pl = fmaf(t2.x, sl, fmaf(t2.y, zh, t2.y) + fmaf(t2.x, zh, -ph));
-  // (t + ph + pl) 2^k as integers of 2^-22 and 2^-44
-  const float h = t2.x * sc, p = ph * sc, l = pl * sc;
-  const float e1 = p + l;
-  const float eh = h + e1;
-  const float el = (e1 - (eh - h)) + (l - (e1 - p));
-  const float i1 = eh + 2.0f;
-  const float i2 = ((eh - (i1 - 2.0f)) + el) + 0x1.8p-21f;
-  const int a = __float_as_int(i1) - __float_as_int(2.0f), b = __float_as_int(i2) - __float_as_int(0x1.8p-21f);
-  return (static_cast<unsigned long long>(static_cast<unsigned int>(a)) << 22) + static_cast<long long>(b);
-}
-
 // log of logit x's share of a mass (by one thread of a row: float64).
-__device__ __forceinline__ float log_share(const RowWeights& r, float x, float T, unsigned long long total) {
-  const double z = (static_cast<double>(x) - static_cast<double>(r.sh)) * temperature_scale(T) - static_cast<double>(r.mo);
-  return static_cast<float>(z * 0.021660849392498290 - log(static_cast<double>(total) * (1.0 / static_cast<double>(1ull << kWeightBits))));
+template <int B>
+__device__ __forceinline__ float log_share(const RowWeights<B>& r, float x, float T, unsigned long long total) {
+  const double z = (static_cast<double>(x) - static_cast<double>(r.sh)) * temperature_scale<B>(T) - static_cast<double>(r.mo);
+  return static_cast<float>(z * (0.69314718055994531 / (1 << B)) -
+                            log(static_cast<double>(total) * (1.0 / static_cast<double>(1ull << kWeightBits))));
 }
 
 constexpr int kSampleThreads = 1024;
@@ -294,9 +343,9 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_logits_kernel(const 
         }
       }
     }
-    sh.tab[t] = kPow32[t >> 5];
+    sh.tab[t] = kPow128[(t >> 5) * 4];
     if (t == kSampleThreads - 1) {
-      const double c = temperature_scale(T);
+      const double c = temperature_scale<5>(T);
       sh.scale[0] = static_cast<float>(c);
       sh.scale[1] = static_cast<float>(c - static_cast<double>(sh.scale[0]));
     }
@@ -341,8 +390,7 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_logits_kernel(const 
     __syncthreads();
   }
   const float mx = key_logit(max_key);
-  const RowWeights rw =
-      row_weights(mx, sh.scale[0], sh.scale[1], needs_shift(mx, sh.scale[0]) ? mx : 0.0f, 1600.0f / sh.scale[0]);
+  const RowWeights<5> rw = row_weights<5>(mx, sh.scale[0], sh.scale[1]);
   const int top_k = a.top_k ? a.top_k[row] : 0;
   const float top_p = a.top_p ? a.top_p[row] : 1.0f, min_p = a.min_p ? a.min_p[row] : 0.0f;
   bool cut_k = top_k > 0 && top_k < a.vocab, cut_p = top_p < 1.0f;
@@ -664,12 +712,17 @@ constexpr int kPlainThreads = 256;
 constexpr int kPlainTile = 512;  // tokens of a warp's tile
 constexpr int kPlainMaxTiles = kMaxSampleVocab / kPlainTile;
 
+// The row is read from HBM for its tiles' maxima and again, mostly from L2,
+// for their sums; the tile that holds the sampled mass a third time.  Tiles
+// whose largest weight is below 2^-9 of the row's -- most of them, in a model's
+// rows -- take the shorter form of the weights: their errors, relative to the
+// row's mass, stay as far below a token's share.
 __global__ void __launch_bounds__(kPlainThreads, 4) sample_plain_kernel(const SampleRowArgs a) {
   constexpr int W = kPlainThreads / 32, E = kPlainTile / 32;
-  __shared__ float2 table[32 * 32];
+  __shared__ float2 table[128 * 32];
   __shared__ unsigned long long tile_sum[kPlainMaxTiles];
-  __shared__ float tile_mo[kPlainMaxTiles];  // the power of two that a tile's sum is against (32nds of an octave)
-  __shared__ unsigned long long xch[3][kSampleMaxCluster], red[W];
+  __shared__ float tile_max[kPlainMaxTiles];
+  __shared__ unsigned long long xch[2][kSampleMaxCluster], red[W];
   __shared__ float scale[2];
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, cs = a.cs;
   const int row = static_cast<int>(blockIdx.x) / cs, rank = static_cast<int>(blockIdx.x) % cs;
@@ -677,17 +730,7 @@ __global__ void __launch_bounds__(kPlainThreads, 4) sample_plain_kernel(const Sa
   const float* src = a.logits + row * a.ld + id0;
   const float T = a.temperature ? a.temperature[row] : 1.0f;
   if (cs > 1) cluster_arrive();
-  for (int i = t; i < 32 * 32; i += kPlainThreads) table[i] = kPow32[i >> 5];
-  if (t == 0) {
-    const double c = temperature_scale(T);
-    scale[0] = static_cast<float>(c);
-    scale[1] = static_cast<float>(c - static_cast<double>(scale[0]));
-  }
-  const float2* tab = table + lane;
-  if (cs > 1) cluster_wait();
-  else __syncthreads();
-  __syncthreads();
-  // every rank's value, for all threads of all ranks; buffers in turn
+  // every rank's value, for all threads of all ranks; a buffer for each use
   auto exchange = [&](int buf, unsigned long long v) -> const unsigned long long* {
     if (cs > 1) {
       if (t < cs) st_dsmem_u64(mapa_shared(smem_u32(&xch[buf][rank]), t), v);
@@ -697,18 +740,6 @@ __global__ void __launch_bounds__(kPlainThreads, 4) sample_plain_kernel(const Sa
       __syncthreads();
     }
     return xch[buf];
-  };
-  auto block_max = [&](unsigned long long v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const unsigned long long y = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-      v = y > v ? y : v;
-    }
-    __syncthreads();
-    if (lane == 0) red[warp] = v;
-    __syncthreads();
-    for (int w = 0; w < W; ++w) v = red[w] > v ? red[w] : v;
-    return v;
   };
   const int tiles = (n + kPlainTile - 1) / kPlainTile;
   const bool aligned = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
@@ -731,175 +762,159 @@ __global__ void __launch_bounds__(kPlainThreads, 4) sample_plain_kernel(const Sa
       }
     }
   };
-  // id within the slice of element e of tile q as load() deals them
-  auto id_of = [&](int q, int e) {
-    const int base = q * kPlainTile;
-    return base + (aligned && base + kPlainTile <= n ? ((e / 4) * 32 + lane) * 4 + (e & 3) : e * 32 + lane);
-  };
-  if (!(T > 0.0f)) {  // the largest logit, lowest id first
-    unsigned long long best = 0;
-    for (int q = warp; q < tiles; q += W) {
-      float x[E];
-      load(q, x);
+  // the largest logit; where it is all that is asked for, with its lowest id
+  const bool greedy = !(T > 0.0f);
+  unsigned long long best = 0;
+#pragma unroll 1
+  for (int q = warp; q < tiles; q += W) {
+    float x[E], m = -INFINITY;
+    load(q, x);
+#pragma unroll
+    for (int e = 0; e < E; ++e) m = fmaxf(m, x[e]);  // (drops NaN)
+    const uint32_t key = __reduce_max_sync(0xFFFFFFFFu, logit_key(m));
+    if (lane == 0) tile_max[q] = key ? key_logit(key) : -INFINITY;
+    uint32_t low = 0;
+    if (greedy) {
+      const int base = q * kPlainTile;
+      const bool by4 = aligned && base + kPlainTile <= n;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const uint32_t k = logit_key(x[e]);
-        const unsigned long long v =
-            k ? (static_cast<unsigned long long>(k) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id0 + id_of(q, e))) : 0;
-        best = v > best ? v : best;
+        const int i = base + (by4 ? ((e / 4) * 32 + lane) * 4 + (e & 3) : e * 32 + lane);
+        if (key && logit_key(x[e]) == key) low = max(low, 0xFFFFFFFFu - static_cast<uint32_t>(id0 + i));
       }
+      low = __reduce_max_sync(0xFFFFFFFFu, low);
     }
-    best = block_max(best);
+    const unsigned long long v = (static_cast<unsigned long long>(key) << 32) | low;
+    best = key && v > best ? v : best;
+  }
+  for (int i = t; i < 128 * 32; i += kPlainThreads) table[i] = kPow128[i >> 5];
+  if (t == 0) {
+    const double c = temperature_scale<7>(T);
+    scale[0] = static_cast<float>(c);
+    scale[1] = static_cast<float>(c - static_cast<double>(scale[0]));
+  }
+  if (lane == 0) red[warp] = best;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < W; ++w) best = red[w] > best ? red[w] : best;
+  if (cs > 1) {
+    cluster_wait();
     const unsigned long long* all = exchange(0, best);
     for (int r = 0; r < cs; ++r) best = all[r] > best ? all[r] : best;
+  }
+  if (best == 0 || greedy) {  // the cluster alike
     if (rank == 0 && t == 0) {
       a.tokens[row] = best ? static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(best)) : -1;
       if (a.logprob) a.logprob[row] = best ? 0.0f : -INFINITY;
     }
     return;
   }
-  const float ch = scale[0], cl = scale[1], drop = 1600.0f / ch;
-  // Once over the row; a second time, shifted by the row's maximum, where some tile's values are too large for the first.
-  float shift = 0.0f;
-  bool infinite = false;  // then the infinite logits share the mass: zeros among nothing
-  auto prepared = [&](float x) { return infinite ? (x == INFINITY ? 0.0f : -INFINITY) : fmaxf(x, -INFINITY); };  // NaN: -inf
-  uint32_t top = 0;
-  float mo = 0.0f;
+  float mx = key_logit(static_cast<uint32_t>(best >> 32));
+  const bool infinite = mx == INFINITY;  // then the infinite logits share the mass: zeros among nothing
+  if (infinite) mx = 0.0f;
+  const RowWeights<7> rw = row_weights<7>(mx, scale[0], scale[1]);
+  const float2* tab = table + lane;
+  // x' of a tile's logits
+  auto shifted = [&](float* x) {
+    if (infinite) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = x[e] == INFINITY ? 0.0f : rw.low;
+    } else if (rw.sh != 0.0f) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = fmaxf(x[e] - rw.sh, rw.low);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = fmaxf(x[e], rw.low);
+    }
+  };
+  auto top_of = [&](int q) { return infinite ? (tile_max[q] == INFINITY ? 0.0f : -INFINITY) : tile_max[q]; };
+  auto is_fine = [&](int q) { return (top_of(q) - mx) * rw.ch > -9.0f * 128.0f; };
 #pragma unroll 1
-  for (int pass = 0;; ++pass) {
-    uint32_t my_top = 0;
-    bool large = false;
-    float my_mo = -INFINITY;
-#pragma unroll 1
-    for (int q = warp; q < tiles; q += W) {
+  for (int q = warp; q < tiles; q += W) {
+    unsigned long long sum = 0;
+    if (top_of(q) - rw.sh > rw.low) {
       float x[E];
       load(q, x);
-      float m = -INFINITY;
+      shifted(x);
+      uint32_t a1 = 0, a2 = 0;  // sums of the bits, modulo 2^32: a tile's steps stay below 2^31
+      if (is_fine(q)) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        x[e] = prepared(x[e]);
-        m = fmaxf(m, x[e]);
+        for (int e = 0; e < E; ++e) {
+          float i1, i2;
+          weight_parts<7, true>(rw, x[e], tab, &i1, &i2);
+          a1 += __float_as_uint(i1);
+          a2 += __float_as_uint(i2);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          float i1, i2;
+          weight_parts<7, false>(rw, x[e], tab, &i1, &i2);
+          a1 += __float_as_uint(i1);
+          a2 += __float_as_uint(i2);
+        }
       }
-      const uint32_t key = __reduce_max_sync(0xFFFFFFFFu, logit_key(m));
-      const float mx = key_logit(key);
-      my_top = max(my_top, key);
-      unsigned long long sum = 0;
-      float t_mo = -INFINITY;
-      if (key && (mx - shift) * ch > -2097152.0f && !needs_shift(mx - shift, ch)) {
-        const RowWeights rw = row_weights(mx, ch, cl, shift, drop);
-#pragma unroll
-        for (int e = 0; e < E; ++e) sum += row_weight(rw, x[e], tab);
-        t_mo = rw.mo;
-      } else if (key && pass == 0) {
-        large = true;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-      if (lane == 0) {
-        tile_sum[q] = sum;
-        tile_mo[q] = t_mo;
-      }
-      my_mo = fmaxf(my_mo, t_mo);
+      a1 = __reduce_add_sync(0xFFFFFFFFu, a1 - static_cast<uint32_t>(E) * __float_as_uint(2.0f));
+      a2 = __reduce_add_sync(0xFFFFFFFFu, a2 - static_cast<uint32_t>(E) * __float_as_uint(kStep44));
+      sum = (static_cast<unsigned long long>(a1) << 22) + static_cast<long long>(static_cast<int32_t>(a2));
     }
-    // (flag, largest key) and the largest power of two
-    const unsigned long long v = block_max((static_cast<unsigned long long>(my_top) << 1) | (large ? 1 : 0));
-    const bool cta_large = __syncthreads_or(large);
-    const unsigned long long* all = exchange(0, (v & ~1ull) | (cta_large ? 1 : 0));
-    bool again = false;
-    top = 0;
-    for (int r = 0; r < cs; ++r) {
-      top = max(top, static_cast<uint32_t>(all[r] >> 1));
-      again = again || (all[r] & 1);
-    }
-    const unsigned long long mv = block_max(my_mo == -INFINITY ? 0 : float_order_key(my_mo));
-    const unsigned long long* mos = exchange(1, mv);
-    uint32_t mk = 0;
-    for (int r = 0; r < cs; ++r) mk = max(mk, static_cast<uint32_t>(mos[r]));
-    mo = key_logit(mk);
-    if (!again || pass == 1 || top == 0) break;
-    shift = key_logit(top);
-    if (shift == INFINITY) {
-      infinite = true;
-      shift = 0.0f;
-    }
-  }
-  if (top == 0) {  // nothing to sample (the cluster alike)
-    if (rank == 0 && t == 0) {
-      a.tokens[row] = -1;
-      if (a.logprob) a.logprob[row] = -INFINITY;
-    }
-    return;
-  }
-  // the tiles' sums against the row's power of two; a run of them per thread, in order
-  auto octaves = [&](int q) { return tile_mo[q] == -INFINITY ? 63 : min(63, static_cast<int>(mo - tile_mo[q]) >> 5); };
-  const int run_len = (tiles + kPlainThreads - 1) / kPlainThreads, q0 = min(tiles, t * run_len), q1 = min(tiles, q0 + run_len);
-  unsigned long long mine = 0;
-  for (int q = q0; q < q1; ++q) mine += tile_sum[q] >> octaves(q);
-  unsigned long long c = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, c, o);
-    if (lane >= o) c += y;
+    if (lane == 0) tile_sum[q] = sum;
   }
   __syncthreads();
+  // a run of tiles per thread, in order
+  const int run_len = (tiles + kPlainThreads - 1) / kPlainThreads, q0 = min(tiles, t * run_len), q1 = min(tiles, q0 + run_len);
+  unsigned long long mine = 0;
+  for (int q = q0; q < q1; ++q) mine += tile_sum[q];
+  const unsigned long long c = warp_scan(mine, lane);
   if (lane == 31) red[warp] = c;
   __syncthreads();
   unsigned long long before = c - mine, own = 0;
+#pragma unroll
   for (int w = 0; w < W; ++w) {
     if (w < warp) before += red[w];
     own += red[w];
   }
-  const unsigned long long* all = exchange(2, own);
+  const unsigned long long* all = exchange(1, own);
   unsigned long long total = 0;
   for (int r = 0; r < cs; ++r) {
     if (r < rank) before += all[r];
     total += all[r];
   }
   const unsigned long long goal = max(1ull, share_of(total, a.u[row]));
-  const bool hit = before < goal && goal <= before + mine;
-  if (!__any_sync(0xFFFFFFFFu, hit)) return;  // (no rank looks into another's memory from here on)
+  const uint32_t hit = __ballot_sync(0xFFFFFFFFu, before < goal && goal <= before + mine);
+  if (!hit) return;  // another warp's (no rank looks into another's memory from here on)
   // this warp finds the tile, reads it again and finds the token
-  int q = 0;
-  unsigned long long left = 0;
-  if (hit) {
-    for (q = q0; q < q1 - 1; ++q) {
-      const unsigned long long s = tile_sum[q] >> octaves(q);
-      if (goal <= before + s) break;
-      before += s;
-    }
-    left = goal - before;
-  }
-  const int who = __ffs(__ballot_sync(0xFFFFFFFFu, hit)) - 1;
-  q = __shfl_sync(0xFFFFFFFFu, q, who);
-  left = __shfl_sync(0xFFFFFFFFu, left, who);
-  left <<= octaves(q);  // in the tile's own units: at most its sum
-  float x[E], m = -INFINITY;
+  const int who = __ffs(hit) - 1;
+  int q = __shfl_sync(0xFFFFFFFFu, q0, who);
+  unsigned long long run = __shfl_sync(0xFFFFFFFFu, before, who);
+  for (; goal > run + tile_sum[q]; ++q) run += tile_sum[q];
+  float x[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int i = q * kPlainTile + lane * E + e;
-    x[e] = i < n ? prepared(src[i]) : -INFINITY;
-    m = fmaxf(m, x[e]);
+    x[e] = i < n ? src[i] : -INFINITY;
   }
-  const float mx = key_logit(__reduce_max_sync(0xFFFFFFFFu, logit_key(m)));
-  const RowWeights rw = row_weights(mx, ch, cl, shift, drop);
-  unsigned long long sum = 0;
+  shifted(x);
+  unsigned long long w[E], sum = 0;
+  const bool fine = is_fine(q);
 #pragma unroll
-  for (int e = 0; e < E; ++e) sum += row_weight(rw, x[e], tab);
-  unsigned long long pre = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, pre, o);
-    if (lane >= o) pre += y;
+  for (int e = 0; e < E; ++e) {
+    float i1, i2;
+    if (fine) weight_parts<7, true>(rw, x[e], tab, &i1, &i2);
+    else weight_parts<7, false>(rw, x[e], tab, &i1, &i2);
+    w[e] = (static_cast<unsigned long long>(__float_as_uint(i1) - __float_as_uint(2.0f)) << 22) +
+           static_cast<long long>(__float_as_int(i2) - __float_as_int(kStep44));
+    sum += w[e];
   }
-  pre -= sum;
-  if (pre < left && left <= pre + sum) {
+  run += warp_scan(sum, lane) - sum;
+  if (run < goal && goal <= run + sum) {
     int found = 0;
     float xf = 0.0f;
     bool done = false;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      pre += row_weight(rw, x[e], tab);
-      if (!done && left <= pre) {
+      run += w[e];
+      if (!done && goal <= run) {
         done = true;
         found = e;
         xf = x[e];
@@ -907,9 +922,9 @@ __global__ void __launch_bounds__(kPlainThreads, 4) sample_plain_kernel(const Sa
     }
     a.tokens[row] = id0 + q * kPlainTile + lane * E + found;
     if (a.logprob) {
-      RowWeights rr = rw;
-      rr.mo = mo;
-      a.logprob[row] = log_share(rr, xf, T, total);
+      RowWeights<7> r = rw;
+      r.sh = 0.0f;  // xf is shifted
+      a.logprob[row] = log_share(r, xf, T, total);
     }
   }
 }

@@ -49,7 +49,7 @@ vsd_status launch_sample(SampleRowArgs& a, cudaStream_t st) {
   CK(cudaGetDevice(&dev));
   CK(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   a.cs = 1;
-  if (!a.top_k && !a.top_p && !a.min_p) {
+  if (!a.top_k && !a.top_p && !a.min_p && static_cast<int64_t>(a.rows) * kSampleMaxCluster > sms) {
     static const int want = getenv("SP_W") ? atoi(getenv("SP_W")) : 12;
     // no filter on any row: streamed; CTAs per row so that the SMs' shares come out even
     while (a.cs < kSampleMaxCluster && static_cast<int64_t>(a.rows) * a.cs < want * sms && a.vocab > a.cs * 4 * kPlainTile) a.cs *= 2;
