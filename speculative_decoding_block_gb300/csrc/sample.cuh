@@ -137,6 +137,12 @@ __device__ __forceinline__ RowWeights<B> row_weights(float mx, float ch, float c
   return r;
 }
 
+// A table entry for a row: the power's exponent holds the row's N already.
+template <int B>
+__device__ __forceinline__ float2 row_power(const RowWeights<B>& r, float2 p) {
+  return make_float2(__int_as_float(__float_as_int(p.x) - (r.n_off << (23 - B))), p.y);
+}
+
 // Weight of x' = max(x - sh, low) as two floats whose bits count steps of 2^-22 above 2 and of 2^-44 above kStep44.
 // tab: this lane's column of the table.  FINE: relative error 2^-36 (B = 5) or 2^-38 (B = 7); else 2^-31 at most and 2^-33 in
 // the mean (B = 7), for weights that are small beside the largest.
@@ -162,17 +168,62 @@ __device__ __forceinline__ void weight_parts(const RowWeights<B>& r, float x, co
     tm = fmaf(x, r.ch, kRoundMagic);
     const float f = fmaf(x, r.cl, fmaf(x, r.ch, -(tm - kRoundMagic)));
     t2 = tab[(__float_as_int(tm) & ((1 << B) - 1)) * 32];
-    const float z = f * kh;
-    s = fmaf(z * z, fmaf(z, 1.0f / 6.0f, 0.5f), z) + t2.y;
+    s = fmaf(f, fmaf(f, fmaf(f, kh * kh * kh / 6.0f, kh * kh / 2.0f), kh), t2.y);
   }
-  // t (1 + s + sl) 2^k, rounded to its steps
-  const float t = __int_as_float(__float_as_int(t2.x) + (((__float_as_int(tm) - r.n_off) >> B) << 23));
-  const float eh = fmaf(t, s, t);
-  float el = fmaf(t, s, t - eh);
-  if (FINE) el = fmaf(t, sl, el);
-  *i1 = eh + 2.0f;
-  *i2 = ((eh - (*i1 - 2.0f)) + el) + kStep44;
+  // t (1 + s + sl), t a power of 2^(1 / 2^B): what lies above 2^-22, and, from the exact t minus that, the rest
+  const float t = __int_as_float(__float_as_int(t2.x) + ((__float_as_int(tm) & -(1 << B)) << (23 - B)));
+  *i1 = fmaf(t, s, t) + 2.0f;
+  float rest = fmaf(t, s, t - (*i1 - 2.0f));
+  if (FINE) rest = fmaf(t, sl, rest);
+  *i2 = rest + kStep44;
 }
+// The short form (B = 7) for two tokens at once, in pairs of f32 operations (the same roundings): their steps' bits are added
+// to a1 and a2.
+__device__ __forceinline__ unsigned long long pair2(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair2(unsigned long long v, uint32_t* a, uint32_t* b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(*a), "=r"(*b) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long fma_2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ unsigned long long add_2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long sub_2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ void weight_steps2(const RowWeights<7>& r, float x0, float x1, const float2* tab, uint32_t* a1, uint32_t* a2) {
+  constexpr float kh = 0x1.62e4300000000p-8f;
+  const unsigned long long x = pair2(x0, x1), ch = pair2(r.ch, r.ch), cl = pair2(r.cl, r.cl), magic = pair2(kRoundMagic, kRoundMagic);
+  const unsigned long long tm = fma_2(x, ch, magic), n = sub_2(magic, tm);  // -N
+  const unsigned long long f = fma_2(x, cl, fma_2(x, ch, n));
+  uint32_t b0, b1;
+  unpair2(tm, &b0, &b1);
+  const float2 p0 = tab[(b0 & 127) * 32], p1 = tab[(b1 & 127) * 32];
+  constexpr float c3 = kh * kh * kh / 6.0f, c2 = kh * kh / 2.0f;
+  const unsigned long long s =
+      fma_2(f, fma_2(f, fma_2(f, pair2(c3, c3), pair2(c2, c2)), pair2(kh, kh)), pair2(p0.y, p1.y));
+  const unsigned long long t = pair2(__uint_as_float(__float_as_uint(p0.x) + ((b0 & ~127u) << 16)),
+                                     __uint_as_float(__float_as_uint(p1.x) + ((b1 & ~127u) << 16)));
+  const unsigned long long two = pair2(2.0f, 2.0f), i1 = add_2(fma_2(t, s, t), two);
+  const unsigned long long i2 = add_2(fma_2(t, s, sub_2(t, sub_2(i1, two))), pair2(kStep44, kStep44));
+  uint32_t u0, u1;
+  unpair2(i1, &u0, &u1);
+  *a1 += u0 + u1;
+  unpair2(i2, &u0, &u1);
+  *a2 += u0 + u1;
+}
+
 // Weight of logit x, in 2^-44.
 template <int B, bool FINE = true>
 __device__ __forceinline__ unsigned long long row_weight(const RowWeights<B>& r, float x, const float2* tab) {
@@ -279,6 +330,7 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_logits_kernel(const 
   if (t == 0) sh.n_list = 0;
   if (cs > 1) cluster_arrive();  // the others' memory is touched once all have started
   const float2* tab = sh.tab + lane;
+  const float2 power = kPow128[(t >> 5) * 4];
 
   auto sync_all = [&]() {
     if (cs > 1) cluster_sync();
@@ -343,7 +395,6 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_logits_kernel(const 
         }
       }
     }
-    sh.tab[t] = kPow128[(t >> 5) * 4];
     if (t == kSampleThreads - 1) {
       const double c = temperature_scale<5>(T);
       sh.scale[0] = static_cast<float>(c);
@@ -391,6 +442,8 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_logits_kernel(const 
   }
   const float mx = key_logit(max_key);
   const RowWeights<5> rw = row_weights<5>(mx, sh.scale[0], sh.scale[1]);
+  sh.tab[t] = row_power(rw, power);
+  __syncthreads();
   const int top_k = a.top_k ? a.top_k[row] : 0;
   const float top_p = a.top_p ? a.top_p[row] : 1.0f, min_p = a.min_p ? a.min_p[row] : 0.0f;
   bool cut_k = top_k > 0 && top_k < a.vocab, cut_p = top_p < 1.0f;
@@ -774,20 +827,19 @@ __global__ void __launch_bounds__(kPlainThreads, 4) sample_plain_kernel(const Sa
     const uint32_t key = __reduce_max_sync(0xFFFFFFFFu, logit_key(m));
     if (lane == 0) tile_max[q] = key ? key_logit(key) : -INFINITY;
     uint32_t low = 0;
-    if (greedy) {
+    if (greedy && key) {
       const int base = q * kPlainTile;
       const bool by4 = aligned && base + kPlainTile <= n;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const int i = base + (by4 ? ((e / 4) * 32 + lane) * 4 + (e & 3) : e * 32 + lane);
-        if (key && logit_key(x[e]) == key) low = max(low, 0xFFFFFFFFu - static_cast<uint32_t>(id0 + i));
+        if (logit_key(x[e]) == key) low = max(low, 0xFFFFFFFFu - static_cast<uint32_t>(id0 + i));
       }
       low = __reduce_max_sync(0xFFFFFFFFu, low);
     }
     const unsigned long long v = (static_cast<unsigned long long>(key) << 32) | low;
     best = key && v > best ? v : best;
   }
-  for (int i = t; i < 128 * 32; i += kPlainThreads) table[i] = kPow128[i >> 5];
   if (t == 0) {
     const double c = temperature_scale<7>(T);
     scale[0] = static_cast<float>(c);
@@ -813,6 +865,8 @@ __global__ void __launch_bounds__(kPlainThreads, 4) sample_plain_kernel(const Sa
   const bool infinite = mx == INFINITY;  // then the infinite logits share the mass: zeros among nothing
   if (infinite) mx = 0.0f;
   const RowWeights<7> rw = row_weights<7>(mx, scale[0], scale[1]);
+  for (int i = t; i < 128 * 32; i += kPlainThreads) table[i] = row_power(rw, kPow128[i >> 5]);
+  __syncthreads();
   const float2* tab = table + lane;
   // x' of a tile's logits
   auto shifted = [&](float* x) {
@@ -829,11 +883,11 @@ __global__ void __launch_bounds__(kPlainThreads, 4) sample_plain_kernel(const Sa
   };
   auto top_of = [&](int q) { return infinite ? (tile_max[q] == INFINITY ? 0.0f : -INFINITY) : tile_max[q]; };
   auto is_fine = [&](int q) { return (top_of(q) - mx) * rw.ch > -9.0f * 128.0f; };
+  float x[E];
 #pragma unroll 1
   for (int q = warp; q < tiles; q += W) {
     unsigned long long sum = 0;
     if (top_of(q) - rw.sh > rw.low) {
-      float x[E];
       load(q, x);
       shifted(x);
       uint32_t a1 = 0, a2 = 0;  // sums of the bits, modulo 2^32: a tile's steps stay below 2^31
@@ -847,12 +901,7 @@ __global__ void __launch_bounds__(kPlainThreads, 4) sample_plain_kernel(const Sa
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          float i1, i2;
-          weight_parts<7, false>(rw, x[e], tab, &i1, &i2);
-          a1 += __float_as_uint(i1);
-          a2 += __float_as_uint(i2);
-        }
+        for (int e = 0; e < E; e += 2) weight_steps2(rw, x[e], x[e + 1], tab, &a1, &a2);
       }
       a1 = __reduce_add_sync(0xFFFFFFFFu, a1 - static_cast<uint32_t>(E) * __float_as_uint(2.0f));
       a2 = __reduce_add_sync(0xFFFFFFFFu, a2 - static_cast<uint32_t>(E) * __float_as_uint(kStep44));
@@ -888,7 +937,6 @@ __global__ void __launch_bounds__(kPlainThreads, 4) sample_plain_kernel(const Sa
   int q = __shfl_sync(0xFFFFFFFFu, q0, who);
   unsigned long long run = __shfl_sync(0xFFFFFFFFu, before, who);
   for (; goal > run + tile_sum[q]; ++q) run += tile_sum[q];
-  float x[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int i = q * kPlainTile + lane * E + e;

@@ -4,7 +4,6 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <cstdlib>
 
 #include "decode_attention.cuh"
 #include "evict.cuh"
@@ -50,7 +49,7 @@ vsd_status launch_sample(SampleRowArgs& a, cudaStream_t st) {
   CK(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   a.cs = 1;
   if (!a.top_k && !a.top_p && !a.min_p && static_cast<int64_t>(a.rows) * kSampleMaxCluster > sms) {
-    static const int want = getenv("SP_W") ? atoi(getenv("SP_W")) : 12;
+    constexpr int want = 8;
     // no filter on any row: streamed; CTAs per row so that the SMs' shares come out even
     while (a.cs < kSampleMaxCluster && static_cast<int64_t>(a.rows) * a.cs < want * sms && a.vocab > a.cs * 4 * kPlainTile) a.cs *= 2;
     a.per = ceil_div_h(ceil_div_h(a.vocab, a.cs), kPlainTile) * kPlainTile;
@@ -58,10 +57,8 @@ vsd_status launch_sample(SampleRowArgs& a, cudaStream_t st) {
     return VSD_OK;
   }
   // CTAs per row: as many as hold its slices, then more while every row still has its SMs at once
-  static const int fcs = getenv("SP_CS") ? atoi(getenv("SP_CS")) : 0;
   while (a.cs < kSampleMaxCluster && (a.vocab > a.cs * 40960 || (static_cast<int64_t>(a.rows) * a.cs * 2 <= sms && a.vocab > a.cs * 2048)))
     a.cs *= 2;
-  if (fcs) a.cs = fcs;
   a.per = (ceil_div_h(a.vocab, a.cs) + 3) / 4 * 4;
   const int smem = static_cast<int>(sizeof(SampleShared)) + (a.per + 4) * 4;
   CK(ensure_smem_opt_in(reinterpret_cast<const void*>(sample_logits_kernel), smem));
