@@ -6,9 +6,14 @@
 // lowest rows; NaN counts as below every number.  Kept rows keep their order
 // and move to rows [0, budget) of the same pages.
 //
-// Moving in place: kept row number j comes from row r_j >= j.  Rows are moved
-// in batches of ascending j, each batch read whole before it is written; a
-// batch writes rows below those that any later batch reads.
+// Bound by the bytes of the kept rows, read and written once.  One CTA (or,
+// where there are few and long ones, a cluster) per (layer, request, KV head):
+// the smallest kept score by three digits of 11, 11 and 10 bits of its ordered
+// key; a bit per row for what stays, with a running count per 32 rows; then the
+// move.  Moving in place: kept row number j comes from row r_j >= j, and rows
+// are moved in batches of ascending j.  A batch writes rows below all that any
+// later batch reads, so only one barrier per batch is needed, between its own
+// reads and its writes, and the next batch's reads are on their way across it.
 #pragma once
 
 #include "vsd_common.cuh"
@@ -17,6 +22,9 @@ namespace vsd {
 
 struct EvictArgs {
   int batch, layers, n_kv, num_pages, ppr, max_tokens, budget, sinks, recent;
+  int cs;            // CTAs per (layer, request, KV head)
+  int words;         // 32-row words of a request at its longest
+  int cache;         // scores kept in shared memory, where a request has no more
   const int* lens;   // [B]
   int* new_lens;     // [B]; nullptr: written by a launch of its own (lens is the same array)
   const int* page_table;
@@ -30,6 +38,11 @@ struct EvictArgs {
 __device__ __forceinline__ uint32_t score_key(float f) { return f != f ? 0u : float_order_key(f + 0.0f); }
 
 constexpr int kEvictThreads = 256;
+constexpr int kEvictBins = 2048;
+constexpr int kEvictWindow = 1024;  // kept rows listed at a time
+constexpr int kEvictMaxCluster = 8;
+constexpr int evict_batch(int hd) { return kEvictThreads * 8 / (2 * (hd / 8)); }  // rows per CTA: eight 16-byte words a thread
+inline int evict_smem_bytes(int words, int cache) { return (kEvictBins + kEvictWindow + 2 * words + cache) * 4; }
 
 // Whether request b's rows [0, L) lie in the pool (every thread of the CTA).
 __device__ __forceinline__ bool pages_ok(const int* pages, int L, int num_pages) {
@@ -43,119 +56,204 @@ __device__ __forceinline__ int evicted_len(int L, int budget, int max_tokens, bo
   return (L >= 0 && L <= max_tokens && ok) ? min(L, budget) : L;
 }
 
-// One CTA per (layer, request, KV head): radix selection of the smallest kept
-// score (four digits of eight bits), then the rows in chunks of 256: keep
-// flags, their running count, and the move.
 template <int HD>
-__global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a) {
-  constexpr int V = HD / 8;                    // 16-byte words of a row
-  constexpr int RB = kEvictThreads * 8 / (2 * V);  // rows moved per batch (8 words a thread)
-  __shared__ int hist[256];
-  __shared__ int warp_cnt[kEvictThreads / 32];
-  __shared__ int src_s[kEvictThreads];
-  __shared__ uint32_t thr_s;
-  __shared__ int need_s;
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const int h = blockIdx.x % a.n_kv, b = (blockIdx.x / a.n_kv) % a.batch, layer = blockIdx.x / a.n_kv / a.batch;
+__global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs a) {
+  constexpr int V = HD / 8;  // 16-byte words of a row
+  constexpr int RB = evict_batch(HD), W = kEvictThreads / 32, U = 8;
+  extern __shared__ __align__(16) uint32_t evict_smem[];
+  uint32_t* hist = evict_smem;
+  int* win = reinterpret_cast<int*>(hist + kEvictBins);
+  uint32_t* mask = reinterpret_cast<uint32_t*>(win + kEvictWindow);  // rows that stay
+  uint32_t* count = mask + a.words;                                  // of them in front of the word (equals' bits before that)
+  float* cache = reinterpret_cast<float*>(count + a.words);
+  __shared__ uint32_t red[W], found[3];
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, cs = a.cs;
+  const int item = static_cast<int>(blockIdx.x) / cs, rank = static_cast<int>(blockIdx.x) % cs;
+  const int h = item % a.n_kv, b = (item / a.n_kv) % a.batch, layer = item / a.n_kv / a.batch;
   const int L = a.lens[b];
   const int* pages = a.page_table + static_cast<size_t>(b) * a.ppr;
   const bool valid = L >= 0 && L <= a.max_tokens;
   const bool ok = valid && pages_ok(pages, L, a.num_pages);
-  if (layer == 0 && h == 0 && t == 0) {
+  if (layer == 0 && h == 0 && rank == 0 && t == 0) {
     if (!valid && L != kIdleSlot) atomicOr(a.status, VSD_DEV_BAD_SEQLEN);
     if (valid && !ok) atomicOr(a.status, VSD_DEV_BAD_PAGE);
     if (a.new_lens) a.new_lens[b] = evicted_len(L, a.budget, a.max_tokens, ok);
   }
-  const size_t head = (static_cast<size_t>(layer) * a.batch + b) * a.n_kv + h;
-  int* kept = a.kept ? a.kept + head * a.budget : nullptr;
-  if (!ok || L <= a.budget) {
-    if (kept)
+  int* kept = a.kept ? a.kept + static_cast<size_t>(item) * a.budget : nullptr;
+  if (!ok || L <= a.budget) {  // the whole cluster alike
+    if (kept && rank == 0)
       for (int j = t; j < a.budget; j += kEvictThreads) kept[j] = (ok && j < L) ? j : -1;
     return;
   }
-  float* score = a.score ? a.score + head * a.max_tokens : nullptr;  // nullptr only where nothing is chosen
+  float* score = a.score ? a.score + static_cast<size_t>(item) * a.max_tokens : nullptr;  // nullptr only where nothing is chosen
   const int mid0 = a.sinks, mid1 = L - a.recent, want = a.budget - a.sinks - a.recent;
-  // the want-th largest key of rows [mid0, mid1), and how many of its equals are kept
-  uint32_t prefix = 0;
-  int need = want;
+  // sum over the threads before this one; all: of all
+  auto block_scan = [&](uint32_t v, uint32_t* all) {
+    uint32_t c = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, c, o);
+      if (lane >= o) c += y;
+    }
+    __syncthreads();
+    if (lane == 31) red[warp] = c;
+    __syncthreads();
+    uint32_t pre = 0, sum = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      pre += w < warp ? red[w] : 0;
+      sum += red[w];
+    }
+    *all = sum;
+    return pre + c - v;
+  };
+
+  // ------------------------------------------------------------------ the want-th largest key of rows [mid0, mid1)
+  uint32_t thr = 0, need = 0, equals = 0;  // kept: keys above thr and the first `need` of its `equals`
+  const bool cached = score && L <= a.cache;
   if (want > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      hist[t] = 0;
+    need = static_cast<uint32_t>(want);
+#pragma unroll 1
+    for (int level = 0; level < 3; ++level) {
+      const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11;
+      for (int i = t; i < kEvictBins; i += kEvictThreads) hist[i] = 0;
       __syncthreads();
-      for (int i = mid0 + t; i < mid1; i += kEvictThreads) {
-        const uint32_t k = score_key(score[i]);
-        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255], 1);
+#pragma unroll 4
+      for (int i = (level == 0 ? 0 : mid0) + t; i < (level == 0 ? L : mid1); i += kEvictThreads) {
+        const float s = level && cached ? cache[i] : score[i];
+        if (!level && cached) cache[i] = s;
+        const uint32_t k = score_key(s);
+        if (i >= mid0 && i < mid1 && (!level || (k >> (shift + bits)) == (thr >> (shift + bits))))
+          atomicAdd(&hist[kEvictBins - 1 - ((k >> shift) & ((1u << bits) - 1))], 1u);  // largest first
       }
       __syncthreads();
-      if (t == 0) {
-        int d = 255, left = need;
-        for (; d > 0 && hist[d] < left; --d) left -= hist[d];
-        thr_s = prefix | (static_cast<uint32_t>(d) << shift);
-        need_s = left;
+      uint32_t n[kEvictBins / kEvictThreads], sum = 0, all;
+#pragma unroll
+      for (int e = 0; e < kEvictBins / kEvictThreads; ++e) sum += n[e] = hist[t * (kEvictBins / kEvictThreads) + e];
+      uint32_t before = block_scan(sum, &all);
+#pragma unroll
+      for (int e = 0; e < kEvictBins / kEvictThreads; ++e) {
+        if (before < need && need <= before + n[e]) {  // one thread
+          found[0] = static_cast<uint32_t>(kEvictBins - 1 - (t * (kEvictBins / kEvictThreads) + e));
+          found[1] = need - before;
+          found[2] = n[e];
+        }
+        before += n[e];
       }
       __syncthreads();
-      prefix = thr_s;
-      need = need_s;
+      thr |= found[0] << shift;
+      need = found[1];
+      equals = found[2];
     }
   }
-  const size_t pool_head = (static_cast<size_t>(layer) * a.num_pages * a.n_kv + h) * kPage * HD;
-  const size_t page_stride = static_cast<size_t>(a.n_kv) * kPage * HD;
-  auto row_ptr = [&](__nv_bfloat16* pool, int i) {
-    return reinterpret_cast<uint4*>(pool + pool_head + pages[i / kPage] * page_stride + (i % kPage) * HD);
-  };
-  int done = 0, ties = 0;  // rows kept and equals of the threshold seen so far
-  for (int i0 = 0; i0 < L; i0 += kEvictThreads) {
-    const int i = i0 + t;
-    const float sc = score && i < L ? score[i] : 0.0f;
+
+  // ------------------------------------------------------------------ what stays, a bit per row
+  const int words = (L + 31) / 32;
+#pragma unroll 2
+  for (int w = warp; w < words; w += W) {
+    const int i = w * 32 + lane;
     const bool in_mid = i >= mid0 && i < mid1;
-    const uint32_t key = score_key(sc);
-    const bool tie = in_mid && want > 0 && key == prefix;
-    // rank of this row among the equals (block-wide running count)
-    const unsigned tb = __ballot_sync(0xFFFFFFFFu, tie);
-    if (lane == 0) warp_cnt[warp] = __popc(tb);
-    __syncthreads();
-    int before = ties, all = 0;
-    for (int w = 0; w < kEvictThreads / 32; ++w) {
-      if (w < warp) before += warp_cnt[w];
-      all += warp_cnt[w];
+    const uint32_t k = want > 0 && in_mid ? score_key(cached ? cache[i] : score[i]) : 0;
+    const bool tie = want > 0 && in_mid && k == thr;
+    const uint32_t ties = __ballot_sync(0xFFFFFFFFu, tie);
+    const uint32_t stay = __ballot_sync(0xFFFFFFFFu, i < L && (!in_mid || (want > 0 && k > thr)));
+    if (lane == 0) {
+      mask[w] = stay | (equals <= need ? ties : 0);
+      count[w] = ties;
     }
-    before += __popc(tb & ((1u << lane) - 1));
-    ties += all;
-    __syncthreads();
-    const bool keep = i < L && (!in_mid || (want > 0 && (key > prefix || (tie && before < need))));
-    const unsigned kb = __ballot_sync(0xFFFFFFFFu, keep);
-    if (lane == 0) warp_cnt[warp] = __popc(kb);
-    __syncthreads();
-    int pos = 0, cnt = 0;
-    for (int w = 0; w < kEvictThreads / 32; ++w) {
-      if (w < warp) pos += warp_cnt[w];
-      cnt += warp_cnt[w];
+  }
+  __syncthreads();
+  const int run = (words + kEvictThreads - 1) / kEvictThreads, w0 = min(words, t * run), w1 = min(words, w0 + run);
+  uint32_t all;
+  if (equals > need) {  // the first ones only
+    uint32_t n = 0;
+    for (int w = w0; w < w1; ++w) n += __popc(count[w]);
+    uint32_t seen = block_scan(n, &all);
+    for (int w = w0; w < w1; ++w) {
+      const uint32_t ties = count[w];
+      uint32_t take = ties;
+      for (int drop = static_cast<int>(seen + __popc(ties)) - static_cast<int>(need); drop > 0 && take; --drop) take &= ~(0x80000000u >> __clz(take));
+      mask[w] |= take;
+      seen += __popc(ties);
     }
-    pos += __popc(kb & ((1u << lane) - 1));
-    if (keep) {
-      src_s[pos] = i;
-      if (kept) kept[done + pos] = i;
+  }
+  uint32_t n = 0;
+  for (int w = w0; w < w1; ++w) n += __popc(mask[w]);
+  uint32_t before = block_scan(n, &all);
+  for (int w = w0; w < w1; ++w) {
+    count[w] = before;
+    before += __popc(mask[w]);
+  }
+  __syncthreads();
+
+  // ------------------------------------------------------------------ the move
+  const size_t pool_head = (static_cast<size_t>(layer) * a.num_pages * a.n_kv + h) * kPage * HD;
+  const size_t page_elems = static_cast<size_t>(a.n_kv) * kPage * HD;
+  auto row_ptr = [&](__nv_bfloat16* pool, int i) {
+    return reinterpret_cast<uint4*>(pool + pool_head + pages[i / kPage] * page_elems + (i % kPage) * HD);
+  };
+  // kept rows [first, first + kEvictWindow) into the window's list
+  auto list = [&](int first) {
+    for (int w = t; w < words; w += kEvictThreads) {
+      uint32_t m = mask[w];
+      int j = static_cast<int>(count[w]) - first;
+      if (j >= kEvictWindow || j + 32 <= 0) continue;
+      for (; m; m &= m - 1, ++j)
+        if (j >= 0 && j < kEvictWindow) {
+          const int i = w * 32 + __ffs(m) - 1;
+          win[j] = i;
+          if (kept && rank == 0) kept[first + j] = i;
+        }
     }
-    __syncthreads();
-    // the chunk's scores were all read above
-    if (keep && score) score[done + pos] = sc;
-    for (int r0 = 0; r0 < cnt; r0 += RB) {
-      uint4 v[8];
+  };
+  struct Batch {
+    uint4 v[U];
+    float s;
+    uint32_t moved;  // bit u: word u has to be written
+  };
+  const int step = cs * RB, steps = (a.budget + step - 1) / step;
+  // this thread's words of batch k: of K and V rows, a score
+  auto read = [&](int k, Batch& x) {
+    const int j0 = k * step + rank * RB;
+    x.moved = 0;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int x = u * kEvictThreads + t, r = r0 + x / (2 * V), c = x % (2 * V);
-        if (r < cnt && src_s[r] != done + r) v[u] = row_ptr(c < V ? a.k_pool : a.v_pool, src_s[r])[c % V];
+    for (int u = 0; u < U; ++u) {
+      const int y = u * kEvictThreads + t, j = j0 + y / (2 * V), c = y % (2 * V);
+      const int src = j < a.budget ? win[j % kEvictWindow] : j;
+      if (src != j) {
+        x.v[u] = row_ptr(c < V ? a.k_pool : a.v_pool, src)[c % V];
+        x.moved |= 1u << u;
       }
-      __syncthreads();
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int x = u * kEvictThreads + t, r = r0 + x / (2 * V), c = x % (2 * V);
-        if (r < cnt && src_s[r] != done + r) row_ptr(c < V ? a.k_pool : a.v_pool, done + r)[c % V] = v[u];
-      }
-      __syncthreads();
     }
-    done += cnt;
-    __syncthreads();
+    if (score && t < RB && j0 + t < a.budget) x.s = score[win[(j0 + t) % kEvictWindow]];
+  };
+  auto write = [&](int k, const Batch& x) {
+    const int j0 = k * step + rank * RB;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int y = u * kEvictThreads + t, j = j0 + y / (2 * V), c = y % (2 * V);
+      if (x.moved >> u & 1) row_ptr(c < V ? a.k_pool : a.v_pool, j)[c % V] = x.v[u];
+    }
+    if (score && t < RB && j0 + t < a.budget) score[j0 + t] = x.s;
+  };
+  Batch cur, next;
+  list(0);
+  __syncthreads();
+  read(0, cur);
+#pragma unroll 1
+  for (int k = 0; k < steps; ++k) {
+    if (k + 1 < steps) {
+      if ((k + 1) * step % kEvictWindow == 0) {
+        __syncthreads();
+        list((k + 1) * step);
+        __syncthreads();
+      }
+      read(k + 1, next);
+    }
+    if (cs > 1) cluster_sync();
+    else __syncthreads();
+    write(k, cur);
+    cur = next;
   }
 }
 
