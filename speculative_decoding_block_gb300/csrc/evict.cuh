@@ -11,9 +11,12 @@
 // the smallest kept score by three digits of 11, 11 and 10 bits of its ordered
 // key; a bit per row for what stays, with a running count per 32 rows; then the
 // move.  Moving in place: kept row number j comes from row r_j >= j, and rows
-// are moved in batches of ascending j.  A batch writes rows below all that any
-// later batch reads, so only one barrier per batch is needed, between its own
-// reads and its writes, and the next batch's reads are on their way across it.
+// are moved in batches of ascending j, which write rows below all that any
+// later batch reads: one barrier per batch is needed, between its own reads
+// and its writes.  More CTAs per SM keep more bytes in flight than reading a
+// batch ahead does (three of 512 threads with four 16-byte words each 221 us,
+// two of 256 with eight words and a batch ahead 278 us for 1.1 GB: 16 requests
+// of 4096 rows cut to 1024, 8 layers, 8 heads of 128).
 #pragma once
 
 #include "vsd_common.cuh"
@@ -37,11 +40,12 @@ struct EvictArgs {
 // Orderable key of a score: NaN lowest, -0 equal to +0.
 __device__ __forceinline__ uint32_t score_key(float f) { return f != f ? 0u : float_order_key(f + 0.0f); }
 
-constexpr int kEvictThreads = 256;
+constexpr int kEvictThreads = 512;
+constexpr int kEvictUnroll = 4;  // 16-byte words of a thread per batch
 constexpr int kEvictBins = 2048;
 constexpr int kEvictWindow = 1024;  // kept rows listed at a time
 constexpr int kEvictMaxCluster = 8;
-constexpr int evict_batch(int hd) { return kEvictThreads * 8 / (2 * (hd / 8)); }  // rows per CTA: eight 16-byte words a thread
+constexpr int evict_batch(int hd) { return kEvictThreads * kEvictUnroll / (2 * (hd / 8)); }  // rows of a CTA's batch
 inline int evict_smem_bytes(int words, int cache) { return (kEvictBins + kEvictWindow + 2 * words + cache) * 4; }
 
 // Whether request b's rows [0, L) lie in the pool (every thread of the CTA).
@@ -57,9 +61,9 @@ __device__ __forceinline__ int evicted_len(int L, int budget, int max_tokens, bo
 }
 
 template <int HD>
-__global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kEvictThreads, 3) evict_kernel(const EvictArgs a) {
   constexpr int V = HD / 8;  // 16-byte words of a row
-  constexpr int RB = evict_batch(HD), W = kEvictThreads / 32, U = 8;
+  constexpr int RB = evict_batch(HD), W = kEvictThreads / 32, U = kEvictUnroll;
   extern __shared__ __align__(16) uint32_t evict_smem[];
   uint32_t* hist = evict_smem;
   int* win = reinterpret_cast<int*>(hist + kEvictBins);
@@ -206,54 +210,38 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
         }
     }
   };
-  struct Batch {
+  const int step = cs * RB;
+#pragma unroll 1
+  for (int first = 0; first < a.budget; first += step) {
+    if (first % kEvictWindow == 0) {
+      __syncthreads();
+      list(first);
+      __syncthreads();
+    }
+    // this thread's words of the batch: of K and V rows, a score
+    const int j0 = first + rank * RB;
     uint4 v[U];
-    float s;
-    uint32_t moved;  // bit u: word u has to be written
-  };
-  const int step = cs * RB, steps = (a.budget + step - 1) / step;
-  // this thread's words of batch k: of K and V rows, a score
-  auto read = [&](int k, Batch& x) {
-    const int j0 = k * step + rank * RB;
-    x.moved = 0;
+    float sc = 0.0f;
+    uint32_t moved = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int y = u * kEvictThreads + t, j = j0 + y / (2 * V), c = y % (2 * V);
       const int src = j < a.budget ? win[j % kEvictWindow] : j;
       if (src != j) {
-        x.v[u] = row_ptr(c < V ? a.k_pool : a.v_pool, src)[c % V];
-        x.moved |= 1u << u;
+        v[u] = row_ptr(c < V ? a.k_pool : a.v_pool, src)[c % V];
+        moved |= 1u << u;
       }
     }
-    if (score && t < RB && j0 + t < a.budget) x.s = score[win[(j0 + t) % kEvictWindow]];
-  };
-  auto write = [&](int k, const Batch& x) {
-    const int j0 = k * step + rank * RB;
+    const bool has_score = score && t < RB && j0 + t < a.budget;
+    if (has_score) sc = score[win[(j0 + t) % kEvictWindow]];
+    if (cs > 1) cluster_sync();
+    else __syncthreads();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int y = u * kEvictThreads + t, j = j0 + y / (2 * V), c = y % (2 * V);
-      if (x.moved >> u & 1) row_ptr(c < V ? a.k_pool : a.v_pool, j)[c % V] = x.v[u];
+      if (moved >> u & 1) row_ptr(c < V ? a.k_pool : a.v_pool, j)[c % V] = v[u];
     }
-    if (score && t < RB && j0 + t < a.budget) score[j0 + t] = x.s;
-  };
-  Batch cur, next;
-  list(0);
-  __syncthreads();
-  read(0, cur);
-#pragma unroll 1
-  for (int k = 0; k < steps; ++k) {
-    if (k + 1 < steps) {
-      if ((k + 1) * step % kEvictWindow == 0) {
-        __syncthreads();
-        list((k + 1) * step);
-        __syncthreads();
-      }
-      read(k + 1, next);
-    }
-    if (cs > 1) cluster_sync();
-    else __syncthreads();
-    write(k, cur);
-    cur = next;
+    if (has_score) score[j0 + t] = sc;
   }
 }
 
