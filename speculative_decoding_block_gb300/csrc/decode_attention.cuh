@@ -153,8 +153,18 @@ __device__ __forceinline__ float new_row_score(const DecodeArgs& a, int b, int h
   return d + __shfl_xor_sync(0xFFFFFFFFu, d, 2);
 }
 
+// What a warp has of a pair: per head (lane / 4) the maximum score, the sum of exponentials against it and the unnormalised
+// output, in the layout of the products' accumulators (rows 0..7: the weights' upper halves; 8..15: the lower ones).
 template <int HD>
-__global__ void __launch_bounds__(kDecThreads, 1) decode_stream_kernel(const DecodeArgs a) {
+struct DecodeAcc {
+  float o[HD / 8][4], m, l;
+  int bad;  // a page outside the pool
+};
+
+// Streams stages [st, st + n_st) of pair (b, h) through the warp's ring; the first stage brings the new row along.
+template <int HD>
+__device__ __forceinline__ void stream_rows(const DecodeArgs& a, const DecodeReq& r, int b, int h, int st, int n_st,
+                                            uint32_t ring_u, uint64_t pol, DecodeAcc<HD>& acc_out) {
   constexpr int SR = dec_stage_rows(HD);  // rows of a stage
   constexpr int PS = SR / kPage;          // pages of a stage
   constexpr int NA = HD / 64;             // 128-byte column blocks of a row
@@ -163,12 +173,174 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_stream_kernel(const Dec
   constexpr int RC = HD / 8;              // 16-byte chunks of a row
   constexpr uint32_t BOX = kPage * 128;   // bytes of a block of 16 rows of 128, 128-byte swizzled
   constexpr uint32_t VOFF = kDecStageBytes / 2;
+  const int lane = threadIdx.x & 31, head = lane >> 2, quad = lane & 3, g = a.group;
+  const bool append = a.k_new != nullptr;
+  const float sl = a.scale_log2;
+  const int row0 = (r.st_lo + st) * SR;
+  const size_t hq = static_cast<size_t>(b) * a.n_q + h * g + (head < g ? head : 0);
+  float (&o)[HD / 8][4] = acc_out.o;
+  float m = -INFINITY, l = 0.0f;
+  int bad = 0;
+#pragma unroll
+  for (int d = 0; d < HD / 8; ++d)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[d][e] = 0.0f;
+  // page-table entries 32 at a time, the next 32 read ahead
+  const int* pages = a.page_table + static_cast<size_t>(b) * a.ppr;
+  const int pg0 = (r.st_lo + st) * PS, page_lo = r.lo / kPage, page_hi = (r.L - 1) / kPage;
+  auto page_block = [&](int blk) { return pages[min(max(pg0 + blk * 32 + lane, page_lo), page_hi)]; };
+  int pg_cur = page_block(0), pg_next = n_st * PS > 32 ? page_block(1) : 0;
+  const size_t layer_head = (static_cast<size_t>(a.layer) * a.num_pages * a.n_kv + h) * kPage * HD + lane * 8;
+  uint32_t qa[KS][2];  // query fragments (rows 8..15 of the tile are zero)
+  // stage i is computed after stage i + kDecStages - 1 has been asked for
+#pragma unroll 1
+  for (int i = -kDecStages; i < n_st; ++i) {
+    if (i >= 0) {
+      cp_async_wait_group<kDecStages - 1>();
+      __syncwarp();
+      const uint32_t kb = ring_u + (i % kDecStages) * kDecStageBytes, vb = kb + VOFF;
+      const int first = row0 + i * SR;
+      // S: s[j][e] = score of row j * 8 + quad * 2 + e for this lane's head, -inf outside the set
+      float s[NT][2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < KS; k += 2) {
+          uint32_t f[4];
+          ldsm_x4(kb + ((j / 2) * NA + k / 4) * BOX + sw128_off((j & 1) * 8 + (lane & 7), (k * 2 & 7) + (lane >> 3)), f);
+          mma_bf16(acc, qa[k][0], 0u, qa[k][1], 0u, f[0], f[1]);
+          mma_bf16(acc, qa[k + 1][0], 0u, qa[k + 1][1], 0u, f[2], f[3]);
+        }
+        s[j][0] = acc[0];
+        s[j][1] = acc[1];
+      }
+      if (first < r.lo || first + SR > r.L) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int row = first + j * 8 + quad * 2 + e;
+            if (row < r.lo || row >= r.L) s[j][e] = -INFINITY;
+          }
+        // V rows outside the set may hold anything, and 0 * NaN is NaN
+#pragma unroll 1
+        for (int y = lane; y < SR * RC; y += 32) {
+          const int row = y / RC, c = y % RC;
+          if (first + row < r.lo || first + row >= r.L)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                             vb + ((row / kPage) * NA + c / 8) * BOX + sw128_off(row % kPage, c % 8)), "r"(0u)
+                         : "memory");
+        }
+        __syncwarp();
+      }
+      if (a.score && head < g) {
+        float* raw = a.raw + hq * a.max_tokens + first + quad * 2;
+        if (first + SR <= a.max_tokens && (a.max_tokens & 1) == 0) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j) *reinterpret_cast<float2*>(raw + j * 8) = make_float2(s[j][0], s[j][1]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (first + j * 8 + quad * 2 + e < a.max_tokens) raw[j * 8 + e] = s[j][e];
+        }
+      }
+      float mx = m;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) mx = fmaxf(mx, fmaxf(s[j][0], s[j][1]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+      const float base = log2_base(mx, sl);
+      if (__any_sync(0xFFFFFFFFu, mx > m)) {
+        const float c = rescale(m, sl, base);
+        l *= c;
+#pragma unroll
+        for (int d = 0; d < HD / 8; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[d][e] *= c;
+      }
+      m = mx;
+      uint32_t ph[NT], pl[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const float p0 = ex2(fmaf(s[j][0], sl, -base)), p1 = ex2(fmaf(s[j][1], sl, -base));
+        l += p0 + p1;
+        ph[j] = f32x2_to_bf16x2(p0, p1);
+        pl[j] = f32x2_to_bf16x2(p0 - __uint_as_float(ph[j] << 16), p1 - __uint_as_float(ph[j] & 0xFFFF0000u));
+      }
+#pragma unroll
+      for (int p = 0; p < PS; ++p) {
+#pragma unroll
+        for (int d = 0; d < HD / 8; d += 2) {
+          uint32_t v[4];
+          ldsm_x4_t(vb + (p * NA + d / 8) * BOX + sw128_off((lane & 7) + ((lane >> 3) & 1) * 8, (d & 7) + (lane >> 4)), v);
+          mma_bf16(o[d], ph[2 * p], pl[2 * p], ph[2 * p + 1], pl[2 * p + 1], v[0], v[1]);
+          mma_bf16(o[d + 1], ph[2 * p], pl[2 * p], ph[2 * p + 1], pl[2 * p + 1], v[2], v[3]);
+        }
+      }
+      __syncwarp();
+    }
+    const int ni = i + kDecStages;
+    if (ni < n_st) {
+      if (((ni * PS) & 31) == 0 && ni) {
+        pg_cur = pg_next;
+        if (ni * PS + 32 < n_st * PS) pg_next = page_block(((ni * PS) >> 5) + 1);
+      }
+      const uint32_t dst = ring_u + (ni % kDecStages) * kDecStageBytes;
+#pragma unroll
+      for (int p = 0; p < PS; ++p) {
+        int page = __shfl_sync(0xFFFFFFFFu, pg_cur, ((ni * PS) & 31) + p);
+        if (page < 0 || page >= a.num_pages) {
+          bad = 1;
+          page = 0;
+        }
+        const size_t src = layer_head + page * (static_cast<size_t>(a.n_kv) * kPage * HD);
+#pragma unroll
+        for (int u = 0; u < kPage * RC / 32; ++u) {
+          const int x16 = u * 32 + lane, row = x16 / RC, c = x16 % RC;
+          const uint32_t to = dst + (p * NA + c / 8) * BOX + sw128_off(row, c & 7);
+          cp_async16_hint(to, a.k_pool + src + u * 256, pol);
+          cp_async16_hint(to + VOFF, a.v_pool + src + u * 256, pol);
+        }
+      }
+    }
+    cp_async_commit();
+    if (i == -1) {  // what the products need is read while the first stages travel
+      const __nv_bfloat16* q = a.q + hq * HD;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(q + k * 16 + quad * 2);
+        qa[k][0] = head < g ? src[0] : 0u;
+        qa[k][1] = head < g ? src[4] : 0u;
+      }
+      if (append && st == 0) {
+        // the new row starts the pair's first segment: its weight is 1 against its own score
+        m = new_row_score<HD>(a, b, h, head, quad);
+        l = head < g && quad == 0 ? 1.0f : 0.0f;
+        const __nv_bfloat16* vn = a.v_new + (static_cast<size_t>(b) * a.n_kv + h) * HD;
+#pragma unroll
+        for (int d = 0; d < HD / 8; ++d) {
+          const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(vn + d * 8 + quad * 2));
+          o[d][0] = v.x;
+          o[d][1] = v.y;
+        }
+      }
+    }
+  }
+  acc_out.m = m;
+  acc_out.l = l + __shfl_xor_sync(0xFFFFFFFFu, l, 1);
+  acc_out.l += __shfl_xor_sync(0xFFFFFFFFu, acc_out.l, 2);
+  acc_out.bad = bad;
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kDecThreads, 1) decode_stream_kernel(const DecodeArgs a) {
   extern __shared__ __align__(1024) uint8_t decode_smem[];  // the rings
   __shared__ int off[kDecMaxReqs + 1];
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, head = lane >> 2, quad = lane & 3;
   const int g = a.group;
-  const bool append = a.k_new != nullptr;
-  const float sl = a.scale_log2;
   pdl_launch_dependents();
   pdl_wait();
   if (warp == 0) {
@@ -217,171 +389,77 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_stream_kernel(const Dec
     }
     const DecodeReq r = decode_request<HD>(a, b);
     const int rem = it - off[b], h = rem / r.stages, st = rem - h * r.stages, n_st = min(r.stages - st, it1 - it);
-    const int row0 = (r.st_lo + st) * SR;
-    const size_t hq = static_cast<size_t>(b) * a.n_q + h * g + (head < g ? head : 0);
     it += n_st;
-    float o[HD / 8][4], m = -INFINITY, l = 0.0f;
-    int bad = 0;  // a page outside the pool
-#pragma unroll
-    for (int d = 0; d < HD / 8; ++d)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[d][e] = 0.0f;
-    // page-table entries 32 at a time, the next 32 read ahead
-    const int* pages = a.page_table + static_cast<size_t>(b) * a.ppr;
-    const int pg0 = (r.st_lo + st) * PS, page_lo = r.lo / kPage, page_hi = (r.L - 1) / kPage;
-    auto page_block = [&](int blk) { return pages[min(max(pg0 + blk * 32 + lane, page_lo), page_hi)]; };
-    int pg_cur = page_block(0), pg_next = n_st * PS > 32 ? page_block(1) : 0;
-    const size_t layer_head = (static_cast<size_t>(a.layer) * a.num_pages * a.n_kv + h) * kPage * HD + lane * 8;
-    uint32_t qa[KS][2];  // query fragments (rows 8..15 of the tile are zero)
-    // stage i is computed after stage i + kDecStages - 1 has been asked for
-#pragma unroll 1
-    for (int i = -kDecStages; i < n_st; ++i) {
-      if (i >= 0) {
-        cp_async_wait_group<kDecStages - 1>();
-        __syncwarp();
-        const uint32_t kb = ring_u + (i % kDecStages) * kDecStageBytes, vb = kb + VOFF;
-        const int first = row0 + i * SR;
-        // S: s[j][e] = score of row j * 8 + quad * 2 + e for this lane's head, -inf outside the set
-        float s[NT][2];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int k = 0; k < KS; k += 2) {
-            uint32_t f[4];
-            ldsm_x4(kb + ((j / 2) * NA + k / 4) * BOX + sw128_off((j & 1) * 8 + (lane & 7), (k * 2 & 7) + (lane >> 3)), f);
-            mma_bf16(acc, qa[k][0], 0u, qa[k][1], 0u, f[0], f[1]);
-            mma_bf16(acc, qa[k + 1][0], 0u, qa[k + 1][1], 0u, f[2], f[3]);
-          }
-          s[j][0] = acc[0];
-          s[j][1] = acc[1];
-        }
-        if (first < r.lo || first + SR > r.L) {
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int row = first + j * 8 + quad * 2 + e;
-              if (row < r.lo || row >= r.L) s[j][e] = -INFINITY;
-            }
-          // V rows outside the set may hold anything, and 0 * NaN is NaN
-#pragma unroll 1
-          for (int y = lane; y < SR * RC; y += 32) {
-            const int row = y / RC, c = y % RC;
-            if (first + row < r.lo || first + row >= r.L)
-              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                               vb + ((row / kPage) * NA + c / 8) * BOX + sw128_off(row % kPage, c % 8)), "r"(0u)
-                           : "memory");
-          }
-          __syncwarp();
-        }
-        if (a.score && head < g) {
-          float* raw = a.raw + hq * a.max_tokens + first + quad * 2;
-          if (first + SR <= a.max_tokens && (a.max_tokens & 1) == 0) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j) *reinterpret_cast<float2*>(raw + j * 8) = make_float2(s[j][0], s[j][1]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (first + j * 8 + quad * 2 + e < a.max_tokens) raw[j * 8 + e] = s[j][e];
-          }
-        }
-        float mx = m;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) mx = fmaxf(mx, fmaxf(s[j][0], s[j][1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-        const float base = log2_base(mx, sl);
-        if (__any_sync(0xFFFFFFFFu, mx > m)) {
-          const float c = rescale(m, sl, base);
-          l *= c;
-#pragma unroll
-          for (int d = 0; d < HD / 8; ++d)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[d][e] *= c;
-        }
-        m = mx;
-        uint32_t ph[NT], pl[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const float p0 = ex2(fmaf(s[j][0], sl, -base)), p1 = ex2(fmaf(s[j][1], sl, -base));
-          l += p0 + p1;
-          ph[j] = f32x2_to_bf16x2(p0, p1);
-          pl[j] = f32x2_to_bf16x2(p0 - __uint_as_float(ph[j] << 16), p1 - __uint_as_float(ph[j] & 0xFFFF0000u));
-        }
-#pragma unroll
-        for (int p = 0; p < PS; ++p) {
-#pragma unroll
-          for (int d = 0; d < HD / 8; d += 2) {
-            uint32_t v[4];
-            ldsm_x4_t(vb + (p * NA + d / 8) * BOX + sw128_off((lane & 7) + ((lane >> 3) & 1) * 8, (d & 7) + (lane >> 4)), v);
-            mma_bf16(o[d], ph[2 * p], pl[2 * p], ph[2 * p + 1], pl[2 * p + 1], v[0], v[1]);
-            mma_bf16(o[d + 1], ph[2 * p], pl[2 * p], ph[2 * p + 1], pl[2 * p + 1], v[2], v[3]);
-          }
-        }
-        __syncwarp();
-      }
-      const int ni = i + kDecStages;
-      if (ni < n_st) {
-        if (((ni * PS) & 31) == 0 && ni) {
-          pg_cur = pg_next;
-          if (ni * PS + 32 < n_st * PS) pg_next = page_block(((ni * PS) >> 5) + 1);
-        }
-        const uint32_t dst = ring_u + (ni % kDecStages) * kDecStageBytes;
-#pragma unroll
-        for (int p = 0; p < PS; ++p) {
-          int page = __shfl_sync(0xFFFFFFFFu, pg_cur, ((ni * PS) & 31) + p);
-          if (page < 0 || page >= a.num_pages) {
-            bad = 1;
-            page = 0;
-          }
-          const size_t src = layer_head + page * (static_cast<size_t>(a.n_kv) * kPage * HD);
-#pragma unroll
-          for (int u = 0; u < kPage * RC / 32; ++u) {
-            const int x16 = u * 32 + lane, row = x16 / RC, c = x16 % RC;
-            const uint32_t to = dst + (p * NA + c / 8) * BOX + sw128_off(row, c & 7);
-            cp_async16_hint(to, a.k_pool + src + u * 256, pol);
-            cp_async16_hint(to + VOFF, a.v_pool + src + u * 256, pol);
-          }
-        }
-      }
-      cp_async_commit();
-      if (i == -1) {  // what the products need is read while the first stages travel
-        const __nv_bfloat16* q = a.q + hq * HD;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const uint32_t* src = reinterpret_cast<const uint32_t*>(q + k * 16 + quad * 2);
-          qa[k][0] = head < g ? src[0] : 0u;
-          qa[k][1] = head < g ? src[4] : 0u;
-        }
-        if (append && st == 0) {
-          // the new row starts the pair's first segment: its weight is 1 against its own score
-          m = new_row_score<HD>(a, b, h, head, quad);
-          l = head < g && quad == 0 ? 1.0f : 0.0f;
-          const __nv_bfloat16* vn = a.v_new + (static_cast<size_t>(b) * a.n_kv + h) * HD;
-#pragma unroll
-          for (int d = 0; d < HD / 8; ++d) {
-            const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(vn + d * 8 + quad * 2));
-            o[d][0] = v.x;
-            o[d][1] = v.y;
-          }
-        }
-      }
-    }
-    l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
-    l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
+    DecodeAcc<HD> x;
+    stream_rows<HD>(a, r, b, h, st, n_st, ring_u, pol, x);
     const size_t rec = static_cast<size_t>(gw) + b * a.n_kv + h;
     if (quad == 0) {
-      a.rec_ml[rec * 16 + head] = m;
-      a.rec_ml[rec * 16 + 8 + head] = head < 7 ? l : (bad ? 1.0f : 0.0f);
+      a.rec_ml[rec * 16 + head] = x.m;
+      a.rec_ml[rec * 16 + 8 + head] = head < 7 ? x.l : (x.bad ? 1.0f : 0.0f);
     }
     if (head < g) {
       float* ro = a.rec_o + (rec * g + head) * HD + quad * 2;
 #pragma unroll
       for (int d = 0; d < HD / 8; ++d)
-        *reinterpret_cast<float2*>(ro + d * 8) = make_float2(o[d][0] + o[d][2], o[d][1] + o[d][3]);
+        *reinterpret_cast<float2*>(ro + d * 8) = make_float2(x.o[d][0] + x.o[d][2], x.o[d][1] + x.o[d][3]);
+    }
+  }
+}
+
+// What a joined pair still owes: the log-sum-exp, the new row into the cache, the weights of rows [lo, hi) (of `threads`
+// threads, the new row's and the log-sum-exp by the first warp of the CTA with `first`).  fin: the joined maximum (log2 units)
+// and 1 / sum per head.
+template <int HD>
+__device__ __forceinline__ void settle_pair(const DecodeArgs& a, const DecodeReq& r, int b, int h, size_t to, bool rows, bool reject,
+                                            bool first, int lo, int hi, int threads, const float* fin) {
+  constexpr float kLn2 = 0.69314718f;
+  const int t = threadIdx.x, lane = t & 31, g = a.group, pair = b * a.n_kv + h;
+  const bool append = a.k_new != nullptr;
+  const float sl = a.scale_log2;
+  const size_t hq0 = static_cast<size_t>(b) * a.n_q + h * g;
+  float* score = a.score ? a.score + static_cast<size_t>(pair) * a.max_tokens : nullptr;
+  if (first && t < 32) {
+    const int head = lane >> 2, quad = lane & 3;
+    float s_new = 0.0f;
+    if (append && !reject) {
+      s_new = new_row_score<HD>(a, b, h, head, quad);
+      if (lane < HD / 4) {  // 16 bytes each: K, then V
+        const bool is_v = lane >= HD / 8;
+        const int c = lane % (HD / 8);
+        reinterpret_cast<uint4*>((is_v ? a.v_pool : a.k_pool) + to)[c] =
+            reinterpret_cast<const uint4*>((is_v ? a.v_new : a.k_new) + static_cast<size_t>(pair) * HD)[c];
+      }
+      if (score) {
+        float p = head < g ? (rows ? ex2(fmaf(s_new, sl, -fin[head])) * fin[8 + head] : 1.0f) : 0.0f;
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) p += __shfl_xor_sync(0xFFFFFFFFu, p, w);
+        if (lane == 0) score[r.L] = p;
+      }
+    }
+    if (a.lse && head < g && quad == 0)
+      a.lse[hq0 + head] = reject ? -INFINITY : rows ? (fin[head] - log2f(fin[8 + head])) * kLn2 : s_new * (sl * kLn2);
+  }
+  if (score && !reject && rows) {
+    const float* raw = a.raw + hq0 * a.max_tokens;
+    // two rows a thread at a time (four measured slower: longer once-run code)
+#pragma unroll 1
+    for (int y0 = lo + t; y0 < hi; y0 += 2 * threads) {
+      const int y1 = y0 + threads;
+      const float old0 = score[y0], old1 = y1 < hi ? score[y1] : 0.0f;
+      float s0[kMaxGroup], s1[kMaxGroup], sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kMaxGroup; ++j) {
+        s0[j] = j < g ? __ldcg(raw + static_cast<size_t>(j) * a.max_tokens + y0) : 0.0f;
+        s1[j] = j < g && y1 < hi ? __ldcg(raw + static_cast<size_t>(j) * a.max_tokens + y1) : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < kMaxGroup; ++j)
+        if (j < g) {
+          sum0 += ex2(fmaf(s0[j], sl, -fin[j])) * fin[8 + j];
+          sum1 += ex2(fmaf(s1[j], sl, -fin[j])) * fin[8 + j];
+        }
+      score[y0] = old0 + sum0;
+      if (y1 < hi) score[y1] = old1 + sum1;
     }
   }
 }
@@ -402,7 +480,6 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeA
   const int b = pair / a.n_kv, h = pair % a.n_kv;
   const bool append = a.k_new != nullptr;
   const float sl = a.scale_log2;
-  constexpr float kLn2 = 0.69314718f;
   const DecodeReq r = decode_request<HD>(a, b);
   // the new row's place
   size_t to = 0;
@@ -413,7 +490,6 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeA
     to = (((static_cast<size_t>(a.layer) * a.num_pages + page) * a.n_kv + h) * kPage + r.L % kPage) * HD;
   }
   const size_t hq0 = static_cast<size_t>(b) * a.n_q + h * g;
-  float* score = a.score ? a.score + static_cast<size_t>(pair) * a.max_tokens : nullptr;
   pdl_launch_dependents();
   pdl_wait();
   const int p0 = a.off[b] + h * r.stages;
@@ -424,7 +500,6 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeA
   // this CTA's output elements [e0, e0 + per): a thread has element e and every `parts`-th record from x on
   const int per = (g * HD + a.chunks - 1) / a.chunks;
   const int parts = per >= kJoinThreads ? 1 : kJoinThreads / per, e0 = chunk * per, ne = min(per, g * HD - e0);
-  float s_new = 0.0f;
   bool reject = r.n == 0 || bad_page;
 #pragma unroll 1
   for (int eb = 0; eb < max(1, ne); eb += kJoinThreads) {
@@ -506,51 +581,80 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeA
       a.out[hq0 * HD + e] = __float2half_rn(reject ? 0.0f : acc);  // one rounding, to the GEMM input type
     }
   }
-  if (chunk == 0 && warp == 0) {
-    const int head = lane >> 2, quad = lane & 3;
-    if (append && !reject) {
-      s_new = new_row_score<HD>(a, b, h, head, quad);
-      if (lane < HD / 4) {  // 16 bytes each: K, then V
-        const bool is_v = lane >= HD / 8;
-        const int c = lane % (HD / 8);
-        reinterpret_cast<uint4*>((is_v ? a.v_pool : a.k_pool) + to)[c] =
-            reinterpret_cast<const uint4*>((is_v ? a.v_new : a.k_new) + static_cast<size_t>(pair) * HD)[c];
-      }
-      if (score) {
-        float p = head < g ? (n_rec > 0 ? ex2(fmaf(s_new, sl, -fin[head])) * fin[8 + head] : 1.0f) : 0.0f;
-#pragma unroll
-        for (int w = 4; w < 32; w <<= 1) p += __shfl_xor_sync(0xFFFFFFFFu, p, w);
-        if (lane == 0) score[r.L] = p;
-      }
-    }
-    if (a.lse && head < g && quad == 0)
-      a.lse[hq0 + head] = reject ? -INFINITY : n_rec > 0 ? (fin[head] - log2f(fin[8 + head])) * kLn2 : s_new * (sl * kLn2);
+  // this CTA's rows
+  const int rows = r.L - r.lo, share_rows = ((rows + a.chunks - 1) / a.chunks + 31) / 32 * 32, lo = r.lo + chunk * share_rows;
+  settle_pair<HD>(a, r, b, h, to, n_rec > 0, reject, chunk == 0, lo, min(r.L, lo + share_rows), kJoinThreads, fin);
+}
+
+// The whole call in one launch, where pairs are short or fill the SMs: a CTA per
+// pair, its stages dealt to the eight warps, their parts joined in shared memory.
+template <int HD>
+__global__ void __launch_bounds__(kDecThreads, 1) decode_pair_kernel(const DecodeArgs a) {
+  extern __shared__ __align__(1024) uint8_t decode_smem[];  // the rings, then the warps' outputs
+  __shared__ float ml[kDecWarps][16], fin[16];
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, head = lane >> 2, quad = lane & 3, g = a.group;
+  const int pair = blockIdx.x, b = pair / a.n_kv, h = pair - b * a.n_kv;
+  const float sl = a.scale_log2;
+  pdl_launch_dependents();
+  pdl_wait();
+  const DecodeReq r = decode_request<HD>(a, b);
+  size_t to = 0;
+  bool reject = r.n == 0;
+  if (a.k_new && r.n > 0) {
+    const int page = a.page_table[static_cast<size_t>(b) * a.ppr + r.L / kPage];
+    if (page < 0 || page >= a.num_pages) reject = true;
+    to = (((static_cast<size_t>(a.layer) * a.num_pages + page) * a.n_kv + h) * kPage + r.L % kPage) * HD;
   }
-  if (score && !reject && n_rec > 0) {
-    const float* raw = a.raw + hq0 * a.max_tokens;
-    // this CTA's rows, two a thread at a time
-    const int rows = r.L - r.lo, share_rows = ((rows + a.chunks - 1) / a.chunks + 31) / 32 * 32;
-    const int lo = r.lo + chunk * share_rows, hi = min(r.L, lo + share_rows);
-#pragma unroll 1
-    for (int y0 = lo + t; y0 < hi; y0 += 2 * kJoinThreads) {
-      const int y1 = y0 + kJoinThreads;
-      const float old0 = score[y0], old1 = y1 < hi ? score[y1] : 0.0f;
-      float s0[kMaxGroup], s1[kMaxGroup], sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
-      for (int j = 0; j < kMaxGroup; ++j) {
-        s0[j] = j < g ? __ldcg(raw + static_cast<size_t>(j) * a.max_tokens + y0) : 0.0f;
-        s1[j] = j < g && y1 < hi ? __ldcg(raw + static_cast<size_t>(j) * a.max_tokens + y1) : 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < kMaxGroup; ++j)
-        if (j < g) {
-          sum0 += ex2(fmaf(s0[j], sl, -fin[j])) * fin[8 + j];
-          sum1 += ex2(fmaf(s1[j], sl, -fin[j])) * fin[8 + j];
-        }
-      score[y0] = old0 + sum0;
-      if (y1 < hi) score[y1] = old1 + sum1;
-    }
+  const int st = warp * r.stages / kDecWarps, n_st = (warp + 1) * r.stages / kDecWarps - st;
+  // (the first stage, with the new row, is the first one of a warp that has any)
+  DecodeAcc<HD> x;
+  x.m = -INFINITY;
+  x.l = 0.0f;
+  x.bad = 0;
+  if (n_st > 0)
+    stream_rows<HD>(a, r, b, h, st, n_st, smem_u32(decode_smem + warp * kDecStages * kDecStageBytes), policy_evict_first(), x);
+  if (quad == 0) {
+    ml[warp][head] = x.m;
+    ml[warp][8 + head] = x.l;
   }
+  const bool bad_page = __syncthreads_or(x.bad) || (reject && r.n > 0);  // and every warp is done with its ring
+  reject = reject || bad_page;
+  float* wo = reinterpret_cast<float*>(decode_smem);  // [warp][8][HD]
+  if (n_st > 0) {
+#pragma unroll
+    for (int d = 0; d < HD / 8; ++d)
+      *reinterpret_cast<float2*>(wo + (warp * 8 + head) * HD + d * 8 + quad * 2) =
+          make_float2(x.o[d][0] + x.o[d][2], x.o[d][1] + x.o[d][3]);
+  }
+  if (t < 8) {
+    float mj = -INFINITY, lj = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) mj = fmaxf(mj, ml[w][t]);
+    const float base = log2_base(mj, sl);
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) lj += ml[w][8 + t] * rescale(ml[w][t], sl, base);
+    fin[t] = base;
+    fin[8 + t] = r.stages > 0 ? 1.0f / lj : 1.0f;
+  }
+  if (t == 0) {
+    if (!r.valid && r.L != kIdleSlot) atomicOr(a.status, VSD_DEV_BAD_SEQLEN);
+    if (bad_page) atomicOr(a.status, VSD_DEV_BAD_PAGE);
+  }
+  __syncthreads();
+  for (int i = t; i < g * HD; i += kDecThreads) {
+    const int j = i / HD;
+    float acc = 0.0f;
+    if (!reject && r.stages > 0) {
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w)
+        if (ml[w][j] != -INFINITY) acc += wo[(w * 8 + j) * HD + i % HD] * rescale(ml[w][j], sl, fin[j]);
+      acc *= fin[8 + j];
+    } else if (!reject) {
+      acc = __bfloat162float(a.v_new[static_cast<size_t>(pair) * HD + i % HD]);  // the new row is all
+    }
+    a.out[(static_cast<size_t>(b) * a.n_q + h * g) * HD + i] = __float2half_rn(acc);  // one rounding, to the GEMM input type
+  }
+  settle_pair<HD>(a, r, b, h, to, r.stages > 0, reject, true, r.lo, r.L, kDecThreads, fin);
 }
 
 }  // namespace vsd

@@ -141,22 +141,27 @@ def check_attention(c, layer, append, window, use_score, use_lse=True, stream=No
 HEADS = [(4, 2, 64), (14, 2, 64), (8, 2, 128), (7, 1, 128), (3, 3, 64)]
 
 
+# the most rows that a cache has room for decides how a call's work is dealt out: a CTA per pair, or even shares and a join
+ROOMS = [1008, 8000]
+
+
+@pytest.mark.parametrize("room", ROOMS)
 @pytest.mark.parametrize("append", [True, False])
 @pytest.mark.parametrize("heads", HEADS)
-def test_decode_attention_matches_oracle_over_lengths(heads, append):
+def test_decode_attention_matches_oracle_over_lengths(heads, append, room):
     """Lengths around pages and tiles, an empty request and an idle slot; rows behind the lengths hold NaN."""
     B = require_gpu()
     lens = [0, 1, 15, 16, 17, 31, 32, 33, 63, 65, 127, 130, -1, 500, 1007]
-    c = Cache(B, 2, *heads, lens, 1008, tag=f"len{heads}{append}")
+    c = Cache(B, 2, *heads, lens, room, tag=f"len{heads}{append}")
     check_attention(c, 1, append, 0, True)
 
 
-@pytest.mark.parametrize("window", [1, 5, 16, 33, 100, 5000])
+@pytest.mark.parametrize("window", [1, 5, 16, 33, 100, 5000, 4000])
 @pytest.mark.parametrize("heads", [(14, 2, 64), (8, 2, 128)])
 def test_decode_attention_window(heads, window):
     B = require_gpu()
-    lens = [0, 4, 16, 31, 48, 100, 101, 999]
-    c = Cache(B, 1, *heads, lens, 1000, tag=f"win{heads}")
+    lens = [0, 4, 16, 31, 48, 100, 101, 999] + ([7990, 4100] if window == 4000 else [])
+    c = Cache(B, 1, *heads, lens, 8000 if window == 4000 else 1000, tag=f"win{heads}{window == 4000}")
     # infinities in every row that the window leaves out
     for b, L in enumerate(lens):
         for i in range(0, max(0, L + 1 - window)):
@@ -180,16 +185,17 @@ def test_decode_attention_one_request(heads, L):
     check_attention(c, 0, True, 0, True)
 
 
-@pytest.mark.parametrize("n_b", [40, 200])
-def test_decode_attention_many_requests(n_b):
+@pytest.mark.parametrize("room", [100, 2000])
+@pytest.mark.parametrize("n_b", [40, 76, 200])
+def test_decode_attention_many_requests(n_b, room):
     B = require_gpu()
     lens = [int(x) for x in gen._rng("many", n_b).integers(0, 90, n_b)]
-    c = Cache(B, 1, 14, 2, 64, lens, 100, tag="many")
+    c = Cache(B, 1, 14, 2, 64, lens, room, tag="many")
     check_attention(c, 0, True, 0, True)
 
 
-def test_decode_attention_beyond_the_rows_kept_on_chip():
-    """A context long enough that the weights' second look at the scores cannot keep them all on chip."""
+def test_decode_attention_of_a_very_long_context():
+    """One KV head's 100,001 rows over every warp of the grid: over a thousand records to join."""
     B = require_gpu()
     L, n_q, n_kv, hd = 100_001, 7, 1, 64
     model = tiny_model(B, 1, n_q, n_kv, hd, 131072)
@@ -255,19 +261,20 @@ def test_decode_attention_offsets_beyond_32_bits():
             assert torch.equal(got, k[l, torch.tensor(rows, device="cuda"), h])
 
 
-def test_decode_attention_rejects_bad_requests_and_spares_the_others():
+@pytest.mark.parametrize("room", [112, 8000])
+def test_decode_attention_rejects_bad_requests_and_spares_the_others(room):
     B = require_gpu()
-    c = Cache(B, 1, 14, 2, 64, [100, 50, 40, 60], 112, fill=0.0, tag="bad")
+    c = Cache(B, 1, 14, 2, 64, [100, 50, 40, 60], room, fill=0.0, tag="bad")
     table = c.table.copy()
     table[1, 2] = c.kv.num_pages       # a page of request 1's rows [32, 48)
     table[2, 40 // 16 + 1] = -5        # not among request 2's rows [0, 41)
     B.vsd_kv_set_page_table(c.kv, torch.tensor(table.reshape(-1), device="cuda"))
     assert B.vsd_get_device_status(c.kv) == B.VSD_DEV_BAD_PAGE
-    seq = torch.tensor([112, 50, 40, 60], dtype=torch.int32, device="cuda")  # request 0: no room for its new row
+    seq = torch.tensor([room, 50, 40, 60], dtype=torch.int32, device="cuda")  # request 0: no room for its new row
     q, kn, vn = bf16((4, 14, 64), 2.0, "rq"), bf16((4, 2, 64), 1.0, "rk"), bf16((4, 2, 64), 1.0, "rv")
     out = torch.full((4, 14 * 64), float("nan"), dtype=torch.float16, device="cuda")
     lse = torch.full((4, 14), float("nan"), device="cuda")
-    score = torch.ones((4, 2, 112), device="cuda")
+    score = torch.ones((4, 2, room), device="cuda")
     kp = c.k_pool.clone()
     B.vsd_decode_attention(c.model, c.kv, 0, 4, seq, q, kn, vn, out, score=score, lse=lse)
     torch.cuda.synchronize()
@@ -281,16 +288,17 @@ def test_decode_attention_rejects_bad_requests_and_spares_the_others():
     assert torch.equal(c.k_pool, kp)
 
 
-def test_decode_attention_graph_replay_streams_and_repeat():
-    """Captured and replayed, on another stream, and two calls for different requests at once: the same bits."""
+@pytest.mark.parametrize("room", [1600, 8000])
+def test_decode_attention_graph_replay_streams_and_repeat(room):
+    """Captured and replayed, on another stream: the same bits."""
     B = require_gpu()
-    c = Cache(B, 1, 14, 2, 64, [700, 90, 1500], 1600, tag="graph")
+    c = Cache(B, 1, 14, 2, 64, [700, 90, 1500], room, tag="graph")
     n_b = 3
     q, kn, vn = bf16((n_b, 14, 64), 2.0, "gq"), bf16((n_b, 2, 64), 1.0, "gk"), bf16((n_b, 2, 64), 1.0, "gv")
 
     def call(stream=None):
         out = torch.empty((n_b, 14 * 64), dtype=torch.float16, device="cuda")
-        score = torch.zeros((n_b, 2, 1600), device="cuda")
+        score = torch.zeros((n_b, 2, room), device="cuda")
         B.vsd_decode_attention(c.model, c.kv, 0, n_b, c.seq, q, kn, vn, out, score=score, stream=stream)
         return out, score
 
