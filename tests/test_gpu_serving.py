@@ -579,6 +579,151 @@ def test_sampling_follows_the_distribution_and_repeats_in_a_graph():
     assert torch.equal(tok, first)
 
 
+@pytest.mark.parametrize("vocab", [1, 3, 511, 513, 4099, 32000, 151936])
+def test_sampling_rows_without_filters(vocab):
+    """Enough rows for the streamed form: temperatures of every size, greedy rows among them, flat and peaked logits."""
+    B = require_gpu()
+    rows = 24
+    x = logits(rows, vocab, vocab + 1, std=0.3)
+    x[::3] = logits(rows // 3, vocab, vocab + 2, std=6.0)
+    T = [0.7, 1.0, 1.5, 0.05, 0.0, 0.3, 3.0, 100.0] * 3
+    check_sample(B, x, uniforms(rows, vocab), T=T)
+    check_sample(B, x, uniforms(rows, vocab + 5))
+
+
+def test_sampling_rows_without_filters_odd_values():
+    """Masked, infinite, NaN and huge logits, extreme temperatures and unaligned rows in the streamed form."""
+    B = require_gpu()
+    rows, vocab, inf = 32, 5003, float("inf")
+    wide = torch.full((rows, vocab + 2), inf, device="cuda")
+    x = wide[:, 1: vocab + 1]
+    x.copy_(logits(rows, vocab, 9))
+    x[0] = -inf
+    x[1] = float("nan")
+    x[2, 1:] = -inf
+    x[3, ::2] = -inf
+    x[4, 5] = inf
+    x[5, [3, 4000]] = inf
+    x[6, ::3] = float("nan")
+    x[7] = -3.0e38
+    x[7, [10, 4020]] = 1.0
+    x[8] *= 1e6                       # x / T beyond the first rounding's range: the shifted form
+    x[9] = 3.0e38
+    x[9, 77] = 3.1e38
+    x[10] -= 1e5
+    x[11, 600:] = -inf                # whole tiles of nothing
+    x[12, :4999] = float("nan")
+    for T in (0.9, 0.01, 50.0):
+        tok = check_sample(B, x, uniforms(rows, 4), T=T)
+        assert tok[0] == tok[1] == -1 and tok[2] == 0 and tok[4] == 5 and tok[5] in (3, 4000) and tok[9] == 77
+    tiny, huge = float(np.float32(1e-38)), float(np.float32(3e38))
+    check_sample(B, x, 0.37, T=[tiny, 1e-5, 1e-3, huge, float("inf"), huge, 0.0, -1.0] * 4)
+    tok, lp = run_sample(B, x, 0.5, T=0.0)
+    h = x.double().cpu().numpy()
+    for r in range(rows):
+        assert tok[r] == S.sample_logits(h[r], 0.5, 0.0)[0]
+        assert lp[r] == (-inf if tok[r] < 0 else 0.0)
+    tok, _ = run_sample(B, x[13:], [0.0, -1.0, float("nan"), 1.0, 7.0] + [0.5] * 14, T=1.0)
+    assert tok[:3].tolist() == [0, 0, 0] and (tok >= 0).all()
+
+
+@pytest.mark.parametrize("rows", [1, 5, 40])
+def test_sampling_many_kept_tokens(rows):
+    """Kept sets too large to gather: their border alone is, or, among many equals and beyond the bins, nothing."""
+    B = require_gpu()
+    x = logits(rows, 50257, 31, std=1.0)
+    for a in (dict(k=2000), dict(k=20000), dict(p=0.98), dict(p=0.999), dict(k=20000, p=0.9), dict(k=3000, p=0.5, m=0.001)):
+        check_sample(B, x, uniforms(rows, 7), T=1.3, **a)
+    # coarse logits: thousands of equals at the border
+    for step in (0.5, 2.0):
+        y = (x / step).round() * step
+        for a in (dict(k=3000), dict(k=40000), dict(p=0.9), dict(k=9000, p=0.7), dict(p=0.3, m=0.01), dict(k=1), dict(p=0.0)):
+            check_sample(B, y, uniforms(rows, 8), T=1.1, **a)
+    # a few tokens far above all others: the k-th lies behind the last bin
+    z = x.clone()
+    z[:, [5, 40000]] += 500.0
+    for a in (dict(k=1), dict(k=2), dict(k=3), dict(k=50), dict(k=60000), dict(p=0.9), dict(k=50, p=0.99)):
+        check_sample(B, z, uniforms(rows, 9), T=[0.2, 30.0, 300.0, 1.0, 80.0][0:1] * rows if rows != 5 else [0.2, 30.0, 300.0, 1.0, 80.0], **a)
+
+
+def test_calls_of_two_caches_at_once_and_a_shared_workspace():
+    """Two caches' calls on two streams; a captured call replayed after other calls have used the cache's workspace."""
+    B = require_gpu()
+    rooms = [8000, 900]
+    caches = [Cache(B, 1, 14, 2, 64, [700, 90, 650], room, tag=f"two{room}") for room in rooms]
+    q, kn, vn = bf16((3, 14, 64), 2.0, "tq"), bf16((3, 2, 64), 1.0, "tk"), bf16((3, 2, 64), 1.0, "tv")
+
+    def call(c, out, score, n=3):
+        B.vsd_decode_attention(c.model, c.kv, 0, n, c.seq, q, kn, vn, out, score=score)
+
+    outs = [(torch.empty((3, 14 * 64), dtype=torch.float16, device="cuda"), torch.zeros((3, 2, room), device="cuda")) for room in rooms]
+    for c, (o, s) in zip(caches, outs):
+        call(c, o, s)
+    torch.cuda.synchronize()
+    want = [(o.clone(), s.clone()) for o, s in outs]
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for c, (o, s), st in zip(caches, outs, side):
+            with torch.cuda.stream(st):
+                s.zero_()
+                call(c, o, s)
+    torch.cuda.synchronize()
+    for (o, s), (wo, ws) in zip(outs, want):
+        assert torch.equal(o, wo) and torch.equal(s, ws)
+    graphs = []
+    for c, (o, s) in zip(caches, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(c, o, s)
+        graphs.append(g)
+    for c, g, (o, s), (wo, ws) in zip(caches, graphs, outs, want):
+        other = torch.empty_like(o)
+        call(c, other, None, 1)  # another shape through the same workspace
+        s.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, wo) and torch.equal(s, ws) and torch.equal(other[0], wo[0])
+    assert all(B.vsd_get_device_status(c.kv) == 0 for c in caches)
+
+
+def test_decode_attention_follows_a_verify_step():
+    """A verify step, a decode call and a verify step again on one cache share its workspace: the steps' results are those of
+    a cache on which no decode call was made."""
+    B = require_gpu()
+    from speculative_decoding_block_gb300.target import build_target
+    from tests.gpu_helpers import StepIO
+    from workload import TINY
+    model = build_target(TINY, gen.master_weights(TINY, seed=5), max_positions=4096)[0]
+    k, v = (bf16((TINY.layers, 300, TINY.n_kv, TINY.head_dim), 0.6, "vs", i) for i in range(2))
+    q, kn, vn = bf16((2, TINY.n_q, 64), 1.0, "vq"), bf16((2, TINY.n_kv, 64), 1.0, "vk"), bf16((2, TINY.n_kv, 64), 1.0, "vv")
+    results = []
+    for decode in (False, True):
+        kv = B.vsd_kv_create(model, 2, 2000)
+        for b in range(2):
+            B.vsd_kv_write(kv, b, 0, k, v)
+        io = StepIO(2, [300, 250], [5, 6], [list(range(16)), list(range(16, 32))])
+        got = []
+        for step in range(3):
+            if decode:
+                out = torch.empty((2, TINY.n_q * 64), dtype=torch.float16, device="cuda")
+                B.vsd_decode_attention(model, kv, 1, 2, io.seq, q, kn, vn, out, score=torch.zeros((2, TINY.n_kv, 2000), device="cuda"))
+            B.vsd_verify_step(model, kv, 2, io.seq, io.pending, io.drafts, io.acc, io.out)
+            torch.cuda.synchronize()
+            got += [io.seq.tolist(), io.pending.tolist(), io.acc.tolist(), io.out.tolist()]
+        assert B.vsd_get_device_status(kv) == 0
+        results.append(got)
+    assert results[0] == results[1]
+
+
+def test_eviction_refuses_a_room_beyond_its_bitmap():
+    B = require_gpu()
+    kv = B.vsd_kv_create(tiny_model(B, 1, 1, 1, 64, 1_000_000), 1, 950_000)
+    seq = torch.tensor([10], dtype=torch.int32, device="cuda")
+    with pytest.raises(B.VsdError) as e:
+        B.vsd_kv_evict(kv, 1, seq, torch.zeros_like(seq), torch.zeros((1, 1, 1, 950_000), device="cuda"), 4)
+    assert e.value.status == B.VSD_ERR_UNSUPPORTED
+
+
 # ------------------------------------------------------------------ arguments
 def test_arguments_are_refused():
     B = require_gpu()
