@@ -115,6 +115,8 @@ def code_only(src: str) -> str:
 
 
 SSM_SOURCES = ("replay_ssm.cuh", "replay_ssm.cu")  # the recurrent-state rollback, outside the verify step
+# single-token serving, outside both
+SERVE_SOURCES = ("decode_attention.cuh", "evict.cuh", "kv_view.h", "sample.cuh", "serve.cu")
 
 
 def kernel_source_sha(ssm: bool = False) -> str:
@@ -124,7 +126,7 @@ def kernel_source_sha(ssm: bool = False) -> str:
     h = hashlib.sha256()
     d = os.path.join(ROOT, "speculative_decoding_block_gb300", "csrc")
     for f in sorted(os.listdir(d)):
-        if (f in SSM_SOURCES) != ssm:
+        if (f in SSM_SOURCES) != ssm or f in SERVE_SOURCES:
             continue
         with open(os.path.join(d, f), encoding="utf-8") as fh:
             h.update(f.encode() + code_only(fh.read()).encode())
