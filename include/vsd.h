@@ -453,11 +453,14 @@ vsd_status vsd_kv_get_anchor(const vsd_kv* kv, int32_t batch, float* dst_dev, vs
  * What a request needs next to block verification when one token at a time is
  * produced: attention of its new token over the same paged cache, a cache that
  * can be cut to a budget of rows, and a token drawn from a row of logits.
- * Asynchronous, without allocation or host round trips, so calls may be
- * captured in CUDA graphs.  The attention runs in the cache's workspace: two
- * calls, or a call and a verify or draft step, of one cache must not overlap
- * on the GPU (order them on one stream; different caches are independent).
- * Pointers belong to the current device, which must be the cache's. */
+ * Asynchronous, without host round trips, so calls may be captured in CUDA
+ * graphs; nothing is allocated but the cache's workspace for scores (4 bytes
+ * per query head and row of every slot), by the first call that accumulates
+ * weights (VSD_ERR_ARG if that one is being captured).  The attention runs in
+ * the cache's workspace: two calls, or a call and a verify or draft step, of
+ * one cache must not overlap on the GPU (order them on one stream; different
+ * caches are independent).  Pointers belong to the current device, which must
+ * be the one on which the cache was made (VSD_ERR_ARG). */
 
 /* Device addresses of the cache's K and V pools, BF16
  * [layers][num_pages][n_kv][16][head_dim] (row i of request b: page-table
@@ -483,7 +486,8 @@ vsd_status vsd_kv_pools(const vsd_kv* kv, uint16_t** k_dev, uint16_t** v_dev);
  * rows max(0, n - window) .. n - 1 take part; others are not looked at,
  * whatever they hold.  No row at all gives out = 0 and lse = -inf.  Every
  * sum is in float32 in a fixed order: the same call gives the same bits.
- * q, k_new, v_new and out must be 16-byte aligned (VSD_ERR_ARG).
+ * q, k_new, v_new and out must be 16-byte aligned and out apart from the
+ * others (VSD_ERR_ARG); at most 1024 requests per call (VSD_ERR_UNSUPPORTED).
  * Needs n <= max_tokens_per_req (else VSD_DEV_BAD_SEQLEN) and the pages of
  * the rows that it reads or writes inside the pool (else VSD_DEV_BAD_PAGE): a
  * rejected request, like an idle slot, gets out = 0 and lse = -inf, and
@@ -514,7 +518,9 @@ vsd_status vsd_decode_attention(const vsd_model* m, vsd_kv* kv, int32_t layer, i
  * vsd_verify_step.
  * L_b outside [0, max_tokens_per_req] (VSD_DEV_BAD_SEQLEN; -1, an idle slot,
  * is no error) or a page of rows [0, L_b) outside the pool
- * (VSD_DEV_BAD_PAGE) leaves the request as it was: new_lens = L_b, kept -1. */
+ * (VSD_DEV_BAD_PAGE) leaves the request as it was: new_lens = L_b, kept -1.
+ * A bit and a count per row of the cache's room have to fit in shared memory:
+ * max_tokens_per_req above some 800,000 is refused (VSD_ERR_UNSUPPORTED). */
 vsd_status vsd_kv_evict(vsd_kv* kv, int32_t batch, const int32_t* seq_lens_dev, int32_t* new_lens_dev,
                         float* score_dev, int32_t budget, int32_t sinks, int32_t recent, int32_t* kept_dev,
                         vsd_stream stream);
@@ -539,9 +545,10 @@ vsd_status vsd_kv_evict(vsd_kv* kv, int32_t batch, const int32_t* seq_lens_dev, 
  *   tokens_dev int32 [rows] out: -1 for a row with nothing to sample
  *   logprob_dev optional float32 [rows] out: log of the token's share of the
  *              kept mass (0 for T <= 0, -inf for a row with nothing)
- * Weights are rounded to 2^-44 of the largest and summed as integers, so that
- * a token does not depend on any order of summation.  rows = 0 does nothing;
- * vocab <= 2^18 (VSD_ERR_UNSUPPORTED above). */
+ * Weights have a relative error of 2^-31 at most, are rounded to 2^-44 of a
+ * power of two above the largest and summed as integers, so that a token does
+ * not depend on any order of summation.  rows = 0 does nothing; vocab <= 2^18
+ * (VSD_ERR_UNSUPPORTED above). */
 vsd_status vsd_sample_logits(const float* logits_dev, int32_t rows, int32_t vocab, int64_t ld,
                              const float* temperature_dev, const int32_t* top_k_dev,
                              const float* top_p_dev, const float* min_p_dev, const float* u_dev,

@@ -128,7 +128,8 @@ struct vsd_kv {
   float *attn_o = nullptr, *attn_ml = nullptr;
   int* attn_counters = nullptr;
   size_t attn_items_cap = 0;
-  float* decode_raw = nullptr;  // [max_batch][n_q][max_tokens] scores of the decode attention
+  int device = 0;               // the device that was current when the cache was made
+  float* decode_raw = nullptr;  // [max_batch][n_q][max_tokens] scores of the decode attention (allocated on first use)
   int* decode_off = nullptr;    // [max_batch + 1] first piece of work of each request there
   float* anchor = nullptr;  // [max_batch][H] residual row of the last accepted position (drafter input)
   int* zeros = nullptr;     // [max_batch] zero context lengths (the draft pass reads no cache)
@@ -189,8 +190,21 @@ vsd::KvView vsd::kv_view(const vsd_kv* kv) {
   v.ws_off = kv->decode_off;
   v.ws_floats_o = kv->attn_items_cap * 128 * c.head_dim;
   v.ws_floats_ml = kv->attn_items_cap * 128 * 2;
-  v.ws_raw = kv->decode_raw;
+  v.device = kv->device;
   return v;
+}
+
+vsd_status vsd::kv_raw_scores(vsd_kv* kv, cudaStream_t st, float** out) {
+  if (!kv->decode_raw) {
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    CK(cudaStreamIsCapturing(st, &capture));
+    if (capture != cudaStreamCaptureStatusNone)
+      return fail(VSD_ERR_ARG, "the cache's first call with scores allocates: make it before a capture");
+    vsd_status s = dalloc(&kv->decode_raw, static_cast<size_t>(kv->max_batch) * kv->m->cfg.n_q * kv->max_tokens, false);
+    if (s) return s;
+  }
+  *out = kv->decode_raw;
+  return VSD_OK;
 }
 
 namespace {
@@ -682,6 +696,7 @@ vsd_status vsd_kv_create(const vsd_model* m, int32_t max_batch, int32_t max_toke
     return e;
   };
   kv->m = m;
+  if (cudaGetDevice(&kv->device) != cudaSuccess) return cleanup(fail(VSD_ERR_CUDA, "no CUDA device"));
   kv->max_batch = max_batch;
   kv->max_tokens = max_tokens;
   kv->ppr = ceil_div(max_tokens, kPage);
@@ -729,7 +744,6 @@ vsd_status vsd_kv_create(const vsd_model* m, int32_t max_batch, int32_t max_toke
   if ((s = dalloc(&kv->attn_o, kv->attn_items_cap * 128 * hd, false)) ||
       (s = dalloc(&kv->attn_ml, kv->attn_items_cap * 128 * 2, false)) ||
       (s = dalloc(&kv->attn_counters, static_cast<size_t>(2) * max_batch * c.n_kv)) ||
-      (s = dalloc(&kv->decode_raw, static_cast<size_t>(max_batch) * c.n_q * max_tokens, false)) ||
       (s = dalloc(&kv->decode_off, static_cast<size_t>(max_batch) + 1)))
     return cleanup(s);
   const auto F16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16, BF16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;

@@ -108,7 +108,7 @@ __device__ __forceinline__ DecodeReq decode_request(const DecodeArgs& a, int b) 
   const int more = a.k_new != nullptr ? 1 : 0;
   DecodeReq r;
   r.L = a.lens[b];
-  r.valid = r.L >= 0 && r.L + more <= a.max_tokens;
+  r.valid = r.L >= 0 && r.L <= a.max_tokens - more;
   r.n = r.valid ? r.L + more : 0;
   r.lo = a.window > 0 ? min(max(r.L, 0), max(0, r.n - a.window)) : 0;
   r.st_lo = r.lo / SR;
@@ -341,8 +341,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_stream_kernel(const Dec
   __shared__ int off[kDecMaxReqs + 1];
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, head = lane >> 2, quad = lane & 3;
   const int g = a.group;
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();  // after the wait: what the next kernel reads early (lengths, pages) is then final
   if (warp == 0) {
     int base = 0;
 #pragma unroll 1
@@ -595,8 +595,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_pair_kernel(const Decod
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, head = lane >> 2, quad = lane & 3, g = a.group;
   const int pair = blockIdx.x, b = pair / a.n_kv, h = pair - b * a.n_kv;
   const float sl = a.scale_log2;
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();  // after the wait: what the next kernel reads early (lengths, pages) is then final
   const DecodeReq r = decode_request<HD>(a, b);
   size_t to = 0;
   bool reject = r.n == 0;

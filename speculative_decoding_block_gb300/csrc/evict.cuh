@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kEvictThreads, 3) evict_kernel(const EvictArgs
   int* kept = a.kept ? a.kept + static_cast<size_t>(item) * a.budget : nullptr;
   if (!ok || L <= a.budget) {  // the whole cluster alike
     if (kept && rank == 0)
-      for (int j = t; j < a.budget; j += kEvictThreads) kept[j] = (ok && j < L) ? j : -1;
+      for (int64_t j = t; j < a.budget; j += kEvictThreads) kept[j] = (ok && j < L) ? static_cast<int>(j) : -1;
     return;
   }
   float* score = a.score ? a.score + static_cast<size_t>(item) * a.max_tokens : nullptr;  // nullptr only where nothing is chosen

@@ -9,16 +9,17 @@ namespace vsd {
 struct KvView {
   const vsd_model* model;
   int layers, n_q, n_kv, hd;
-  int max_batch, max_tokens, num_pages, ppr, sms;
+  int device, max_batch, max_tokens, num_pages, ppr, sms;
   __nv_bfloat16 *k_pool, *v_pool;  // [layers][num_pages][n_kv][16][hd]
   const int* page_table;           // [max_batch][ppr]
   int* status;
   // attention workspace (shared with the step): partial outputs, their maxima and sums
   float *ws_o, *ws_ml;
   int* ws_off;    // [max_batch + 1] first piece of work of each request of the decode attention
-  float* ws_raw;  // scores of the decode attention [max_batch][n_q][max_tokens]
   size_t ws_floats_o, ws_floats_ml;
 };
 KvView kv_view(const vsd_kv* kv);
+// The cache's workspace for scores [max_batch][n_q][max_tokens], allocated on the first call (not while `st` is captured).
+vsd_status kv_raw_scores(vsd_kv* kv, cudaStream_t st, float** out);
 
 }  // namespace vsd

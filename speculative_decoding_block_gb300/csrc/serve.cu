@@ -18,6 +18,14 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// The cache's memory, tables and workspace are on the device that was current when it was made.
+vsd_status check_device(const KvView& c) {
+  int dev = -1;
+  CK(cudaGetDevice(&dev));
+  if (dev != c.device) return fail(VSD_ERR_ARG, "the cache is on device %d, the current device is %d", c.device, dev);
+  return VSD_OK;
+}
+
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;
@@ -44,6 +52,7 @@ vsd_status launch_decode(const KvView& c, DecodeArgs& a, cudaStream_t st) {
   }
   // no more CTAs than one stage per warp could use
   const int64_t stages = static_cast<int64_t>(a.batch) * c.n_kv * ceil_div_h(c.max_tokens, dec_stage_rows(HD));
+  if (stages > INT32_MAX) return fail(VSD_ERR_UNSUPPORTED, "%d requests of up to %d rows are too many", a.batch, c.max_tokens);
   const int grid = static_cast<int>(std::min<int64_t>(c.sms, std::max<int64_t>(1, (stages + kDecWarps - 1) / kDecWarps)));
   const int64_t records = static_cast<int64_t>(grid) * kDecWarps + static_cast<int64_t>(a.batch) * c.n_kv;
   if (records * a.group * HD > static_cast<int64_t>(c.ws_floats_o) || records * 16 > static_cast<int64_t>(c.ws_floats_ml))
@@ -122,6 +131,9 @@ vsd_status vsd_decode_attention(const vsd_model* m, vsd_kv* kv, int32_t layer, i
   if (window < 0) return fail(VSD_ERR_ARG, "window %d below 0", window);
   if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(out))
     return fail(VSD_ERR_ARG, "q, k_new, v_new and out must be 16-byte aligned");
+  const size_t q_bytes = static_cast<size_t>(batch) * c.n_q * c.hd * 2, new_bytes = static_cast<size_t>(batch) * c.n_kv * c.hd * 2;
+  if (overlap(out, q_bytes, q, q_bytes) || (k_new && (overlap(out, q_bytes, k_new, new_bytes) || overlap(out, q_bytes, v_new, new_bytes))))
+    return fail(VSD_ERR_ARG, "out must not overlap q, k_new or v_new");
   DecodeArgs a{};
   a.batch = batch;
   a.n_q = c.n_q;
@@ -146,8 +158,10 @@ vsd_status vsd_decode_attention(const vsd_model* m, vsd_kv* kv, int32_t layer, i
   a.rec_o = c.ws_o;
   a.rec_ml = c.ws_ml;
   a.off = c.ws_off;
-  a.raw = c.ws_raw;
   a.status = c.status;
+  vsd_status s = check_device(c);
+  if (s) return s;
+  if (score && (s = kv_raw_scores(kv, reinterpret_cast<cudaStream_t>(stream), &a.raw))) return s;
   return c.hd == 64 ? launch_decode<64>(c, a, reinterpret_cast<cudaStream_t>(stream))
                     : launch_decode<128>(c, a, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -183,8 +197,9 @@ vsd_status vsd_kv_evict(vsd_kv* kv, int32_t batch, const int32_t* seq_lens, int3
   a.kept = kept;
   a.status = c.status;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  vsd_status s = c.hd == 64 ? launch_evict<64>(c, a, st) : launch_evict<128>(c, a, st);
+  vsd_status s = check_device(c);
   if (s) return s;
+  if ((s = c.hd == 64 ? launch_evict<64>(c, a, st) : launch_evict<128>(c, a, st))) return s;
   if (!a.new_lens) {
     evict_lens_kernel<<<batch, kEvictThreads, 0, st>>>(a, new_lens);
     CK(cudaGetLastError());

@@ -288,6 +288,48 @@ def test_decode_attention_rejects_bad_requests_and_spares_the_others(room):
     assert torch.equal(c.k_pool, kp)
 
 
+@pytest.mark.parametrize("append", [True, False])
+@pytest.mark.parametrize("room", [112, 8000])
+def test_decode_attention_rejects_lengths_at_the_type_s_ends(room, append):
+    """2^31 - 1 rows and one more do not wrap around to a valid length."""
+    B = require_gpu()
+    c = Cache(B, 1, 14, 2, 64, [0, 0, 40], room, fill=0.0, tag="ends")
+    seq = torch.tensor([2 ** 31 - 1, -2 ** 31, 40], dtype=torch.int32, device="cuda")
+    q, kn, vn = bf16((3, 14, 64), 2.0, "eq"), bf16((3, 2, 64), 1.0, "ek"), bf16((3, 2, 64), 1.0, "ev")
+    out = torch.full((3, 14 * 64), float("nan"), dtype=torch.float16, device="cuda")
+    lse = torch.full((3, 14), float("nan"), device="cuda")
+    score = torch.ones((3, 2, room), device="cuda")
+    kp = c.k_pool.clone()
+    B.vsd_decode_attention(c.model, c.kv, 0, 3, seq, q, kn if append else None, vn if append else None, out, score=score, lse=lse)
+    torch.cuda.synchronize()
+    assert B.vsd_get_device_status(c.kv) == B.VSD_DEV_BAD_SEQLEN
+    assert not out[:2].any() and torch.isneginf(lse[:2]).all() and (score[:2] == 1).all()
+    assert torch.isfinite(lse[2]).all()
+    if append:
+        kp[0, c.table[2, 40 // 16], :, 40 % 16] = kn[2]
+    assert torch.equal(c.k_pool, kp)
+
+
+def test_first_call_with_scores_is_refused_in_a_capture():
+    """The workspace for scores is allocated by the first call that needs it; the call without scores can be captured at once."""
+    B = require_gpu()
+    c = Cache(B, 1, 4, 2, 64, [30], 64, fill=0.0, tag="first")
+    q, kn, vn = bf16((1, 4, 64), 2.0, "fq"), bf16((1, 2, 64), 1.0, "fk"), bf16((1, 2, 64), 1.0, "fv")
+    out, again = (torch.zeros((1, 256), dtype=torch.float16, device="cuda") for _ in range(2))
+    score = torch.zeros((1, 2, 64), device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.vsd_decode_attention(c.model, c.kv, 0, 1, c.seq, q, kn, vn, out)
+        with pytest.raises(B.VsdError, match="before a capture"):
+            B.vsd_decode_attention(c.model, c.kv, 0, 1, c.seq, q, kn, vn, out, score=score)
+    graph.replay()
+    B.vsd_decode_attention(c.model, c.kv, 0, 1, c.seq, q, kn, vn, again, score=score)
+    torch.cuda.synchronize()
+    assert out.any() and torch.equal(out, again) and not score[:, :, 31:].any()
+    # 4 query heads' weights over 31 rows: each KV head's two sum to 2, of 62 terms within 2^-16 (of the weights' own bound)
+    assert (score.sum(-1) - 2).abs().max() < 2 * (2 ** -16 + 62 * 2 ** -24)
+
+
 @pytest.mark.parametrize("room", [1600, 8000])
 def test_decode_attention_graph_replay_streams_and_repeat(room):
     """Captured and replayed, on another stream: the same bits."""
@@ -724,6 +766,20 @@ def test_eviction_refuses_a_room_beyond_its_bitmap():
     assert e.value.status == B.VSD_ERR_UNSUPPORTED
 
 
+def test_eviction_with_a_budget_of_the_whole_type():
+    """The list of kept rows is filled to its end, past where a 32-bit index of the loop would wrap."""
+    B = require_gpu()
+    budget = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 16 * 2 ** 30:
+        pytest.skip("16 GB of free memory")
+    c = Cache(B, 1, 1, 1, 64, [20], 64, fill=0.0, tag="max")
+    kept, new = torch.zeros((1, 1, 1, budget), dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.vsd_kv_evict(c.kv, 1, c.seq, new, torch.zeros((1, 1, 1, 64), device="cuda"), budget, kept=kept)
+    torch.cuda.synchronize()
+    assert new.tolist() == [20] and kept[0, 0, 0, :20].tolist() == list(range(20))
+    assert int(kept[0, 0, 0, 20:].max()) == -1 and int(kept[0, 0, 0, 20:].min()) == -1
+
+
 # ------------------------------------------------------------------ arguments
 def test_arguments_are_refused():
     B = require_gpu()
@@ -743,6 +799,13 @@ def test_arguments_are_refused():
         assert e.value.status == B.VSD_ERR_ARG, bad
     with pytest.raises(B.VsdError, match="aligned"):
         attend(q=torch.empty(2 * 256 + 1, dtype=torch.bfloat16, device="cuda")[1:])
+    both = bf16((2, 4, 64), 1.0, "ab")
+    with pytest.raises(B.VsdError, match="overlap"):
+        attend(q=both, out=both.view(torch.float16))
+    with pytest.raises(B.VsdError, match="overlap"):
+        attend(k=both.view(-1)[256:].view(2, 2, 64), out=both.view(torch.float16))
+    with pytest.raises(ValueError, match="device"):
+        attend(out=out.cpu())
     with pytest.raises(ValueError):
         attend(batch=3)  # q, out and lengths hold two requests
     with pytest.raises(ValueError):

@@ -101,3 +101,18 @@ def test_sampling_sizes_are_refused_without_a_gpu():
     assert call(1, 8, 7) == binding.VSD_ERR_ARG
     assert call(1, (1 << 18) + 1, 1 << 20) == binding.VSD_ERR_UNSUPPORTED
     assert call(0, 8, 8) == binding.VSD_OK
+
+
+def test_tensors_of_another_device_are_refused():
+    class Fake:
+        def __init__(self, device):
+            self.device = device
+
+        def get_device(self):
+            return self.device
+
+    binding._on_device(0, q=Fake(0), lse=None)
+    with pytest.raises(ValueError, match="out is on device 1"):
+        binding._on_device(0, q=Fake(0), out=Fake(1))
+    with pytest.raises(ValueError, match="u is on device -1"):  # a host tensor
+        binding._on_device(0, u=Fake(-1))
