@@ -253,9 +253,11 @@ __device__ __forceinline__ unsigned long long share_of(unsigned long long total,
   return q + (rest != 0);
 }
 
-// log of logit x's share of a mass (by one thread of a row: float64).
+// log of logit x's share of a mass, w its weight there (by one thread of a row).  A share above half: from the rest, so that
+// a small logarithm keeps its digits and a token alone gets 0; else from the logit itself, in float64.
 template <int B>
-__device__ __forceinline__ float log_share(const RowWeights<B>& r, float x, float T, unsigned long long total) {
+__device__ __forceinline__ float log_share(const RowWeights<B>& r, float x, float T, unsigned long long w, unsigned long long total) {
+  if (total - w < w) return -log1pf(static_cast<float>(total - w) / static_cast<float>(w));
   const double z = (static_cast<double>(x) - static_cast<double>(r.sh)) * temperature_scale<B>(T) - static_cast<double>(r.mo);
   return static_cast<float>(z * (0.69314718055994531 / (1 << B)) -
                             log(static_cast<double>(total) * (1.0 / static_cast<double>(1ull << kWeightBits))));
@@ -598,7 +600,7 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_logits_kernel(const 
             if (kw && ahead < rest && rest <= ahead + kw &&
                 border == min(kSampleList - 1, static_cast<int>(static_cast<float>(id) * (static_cast<float>(kSampleList) / a.vocab)))) {
               a.tokens[row] = id;
-              if (a.logprob) a.logprob[row] = log_share(rw, x, T, total);
+              if (a.logprob) a.logprob[row] = log_share(rw, x, T, kw, total);
             }
             return;
           }
@@ -752,7 +754,7 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_logits_kernel(const 
     if (got) {
       if (lane == __ffs(got) - 1) {
         a.tokens[row] = id0 + i;
-        if (a.logprob) a.logprob[row] = log_share(rw, xs[i], T, total);
+        if (a.logprob) a.logprob[row] = log_share(rw, xs[i], T, w, total);
       }
       break;
     }
@@ -958,6 +960,7 @@ __global__ void __launch_bounds__(kPlainThreads, 4) sample_plain_kernel(const Sa
   if (run < goal && goal <= run + sum) {
     int found = 0;
     float xf = 0.0f;
+    unsigned long long wf = 1;
     bool done = false;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -966,13 +969,14 @@ __global__ void __launch_bounds__(kPlainThreads, 4) sample_plain_kernel(const Sa
         done = true;
         found = e;
         xf = x[e];
+        wf = w[e];
       }
     }
     a.tokens[row] = id0 + q * kPlainTile + lane * E + found;
     if (a.logprob) {
       RowWeights<7> r = rw;
       r.sh = 0.0f;  // xf is shifted
-      a.logprob[row] = log_share(r, xf, T, total);
+      a.logprob[row] = log_share(r, xf, T, wf, total);
     }
   }
 }

@@ -621,6 +621,34 @@ def test_sampling_follows_the_distribution_and_repeats_in_a_graph():
     assert torch.equal(tok, first)
 
 
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("filters", [dict(), dict(k=7), dict(p=1 - 2.0 ** -24)])
+def test_log_probability_of_a_token_alone_or_nearly(rows, filters):
+    """A token alone has a logarithm of exactly 0; one that a little mass stands beside keeps its digits.
+
+    The rest, exp(-gap / T), has a relative error of 2^-31 and a rounding of half a step of 2^-44 against a largest weight of
+    1/2 to 1 (2^-44 relative to that); then four float32 roundings of 2^-24."""
+    B = require_gpu()
+    vocab, inf = 5000, float("inf")
+    g = torch.Generator("cuda").manual_seed(11)
+    x = torch.randn((rows, vocab), device="cuda", generator=g)
+    for T in (0.37, 1.0, 1.7):
+        for one in (dict(k=1), dict(m=1.0), dict(k=1, p=0.5, m=0.1), dict(p=1e-6)):
+            tok, lp = run_sample(B, x, 0.7, T=T, **one)
+            assert (tok == x.argmax(1).cpu().numpy()).all() and (lp == 0).all(), (T, one)
+        y = torch.full((rows, vocab), -inf, device="cuda")
+        y[:, 4321] = 2.5
+        tok, lp = run_sample(B, y, 0.7, T=T, **filters)
+        assert (tok == 4321).all() and (lp == 0).all()
+        for gap in (0.5, 3.0, 9.0, 15.0):
+            y[:, 17] = 2.5 - gap
+            tok, lp = run_sample(B, y, 1 - 2.0 ** -24, T=T, **filters)  # the higher id, whatever its share
+            rest = np.exp(-gap / np.float64(np.float32(T)))
+            want = -np.log1p(rest if "p" not in filters or 1 / (1 + rest) < np.float32(filters["p"]) else 0.0)
+            assert (tok == 4321).all()
+            assert np.abs(lp - want).max() <= abs(want) * (2.0 ** -31 + 2.0 ** -43 / rest + 4 * 2.0 ** -24), (T, gap)
+
+
 @pytest.mark.parametrize("vocab", [1, 3, 511, 513, 4099, 32000, 151936])
 def test_sampling_rows_without_filters(vocab):
     """Enough rows for the streamed form: temperatures of every size, greedy rows among them, flat and peaked logits."""
