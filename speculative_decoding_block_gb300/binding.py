@@ -9,6 +9,7 @@ Loading fails loudly if the shared library is missing: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -177,6 +178,11 @@ def _on_device(device: int, **tensors) -> None:
     for name, t in tensors.items():
         if t is not None and t.get_device() != device:
             raise ValueError(f"{name} is on device {t.get_device()}, the current device is {device}")
+
+
+@functools.cache
+def _several_devices() -> bool:  # with one, _dev's refusal of host tensors is enough, and a small call is bound by the host
+    return torch.cuda.device_count() > 1
 
 
 B16 = (torch.bfloat16, torch.int16, torch.uint16, torch.float16)
@@ -518,7 +524,8 @@ def vsd_decode_attention(model: Model, kv: KV, layer: int, batch: int, seq_lens,
     score: float32 [batch, n_kv, max_tokens], to which the attention weights are added."""
     c = model.cfg
     n_q, n_kv = batch * c.n_q * c.head_dim, batch * c.n_kv * c.head_dim
-    _on_device(torch.cuda.current_device(), seq_lens=seq_lens, q=q, k_new=k_new, v_new=v_new, out=out, score=score, lse=lse)
+    if _several_devices():
+        _on_device(torch.cuda.current_device(), seq_lens=seq_lens, q=q, k_new=k_new, v_new=v_new, out=out, score=score, lse=lse)
     _check(lib().vsd_decode_attention(model.handle, kv.handle, layer, batch, _dev(seq_lens, I32, "seq_lens", batch),
                                       _dev(q, B16, "q", n_q), _dev(k_new, B16, "k_new", n_kv),
                                       _dev(v_new, B16, "v_new", n_kv), int(window),
@@ -534,7 +541,8 @@ def vsd_kv_evict(kv: KV, batch: int, seq_lens, new_lens, score, budget: int, sin
     score: float32 [layers, batch, n_kv, max_tokens]; kept: optional int32 [layers, batch, n_kv, budget]."""
     c = kv.model.cfg
     heads = c.layers * batch * c.n_kv
-    _on_device(torch.cuda.current_device(), seq_lens=seq_lens, new_lens=new_lens, score=score, kept=kept)
+    if _several_devices():
+        _on_device(torch.cuda.current_device(), seq_lens=seq_lens, new_lens=new_lens, score=score, kept=kept)
     _check(lib().vsd_kv_evict(kv.handle, batch, _dev(seq_lens, I32, "seq_lens", batch),
                               _dev(new_lens, I32, "new_lens", batch), _dev(score, F32, "score", heads * kv.max_tokens),
                               int(budget), int(sinks), int(recent), _dev(kept, I32, "kept", heads * max(budget, 0)),
@@ -554,8 +562,9 @@ def vsd_sample_logits(logits, u, tokens, temperature=None, top_k=None, top_p=Non
     ld = logits.stride(0) if rows > 1 else vocab
     if ld < vocab:
         raise ValueError("logits has overlapping rows")
-    _on_device(torch.cuda.current_device(), logits=logits, u=u, tokens=tokens, temperature=temperature, top_k=top_k,
-               top_p=top_p, min_p=min_p, logprob=logprob)
+    if _several_devices():
+        _on_device(torch.cuda.current_device(), logits=logits, u=u, tokens=tokens, temperature=temperature, top_k=top_k,
+                   top_p=top_p, min_p=min_p, logprob=logprob)
     _check(lib().vsd_sample_logits(ctypes.c_void_p(logits.data_ptr()), rows, vocab, ld,
                                    _dev(temperature, F32, "temperature", rows), _dev(top_k, I32, "top_k", rows),
                                    _dev(top_p, F32, "top_p", rows), _dev(min_p, F32, "min_p", rows),

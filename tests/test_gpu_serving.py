@@ -832,7 +832,7 @@ def test_arguments_are_refused():
         attend(q=both, out=both.view(torch.float16))
     with pytest.raises(B.VsdError, match="overlap"):
         attend(k=both.view(-1)[256:].view(2, 2, 64), out=both.view(torch.float16))
-    with pytest.raises(ValueError, match="device"):
+    with pytest.raises(TypeError, match="CUDA"):
         attend(out=out.cpu())
     with pytest.raises(ValueError):
         attend(batch=3)  # q, out and lengths hold two requests
