@@ -947,20 +947,19 @@ __global__ void __launch_bounds__(kPlainThreads, 4) sample_plain_kernel(const Sa
   shifted(x);
   unsigned long long w[E], sum = 0;
   const bool fine = is_fine(q);
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
+  auto weight_of = [&](float v) {
     float i1, i2;
-    if (fine) weight_parts<7, true>(rw, x[e], tab, &i1, &i2);
-    else weight_parts<7, false>(rw, x[e], tab, &i1, &i2);
-    w[e] = (static_cast<unsigned long long>(__float_as_uint(i1) - __float_as_uint(2.0f)) << 22) +
+    if (fine) weight_parts<7, true>(rw, v, tab, &i1, &i2);
+    else weight_parts<7, false>(rw, v, tab, &i1, &i2);
+    return (static_cast<unsigned long long>(__float_as_uint(i1) - __float_as_uint(2.0f)) << 22) +
            static_cast<long long>(__float_as_int(i2) - __float_as_int(kStep44));
-    sum += w[e];
-  }
+  };
+#pragma unroll
+  for (int e = 0; e < E; ++e) sum += w[e] = weight_of(x[e]);
   run += warp_scan(sum, lane) - sum;
   if (run < goal && goal <= run + sum) {
     int found = 0;
     float xf = 0.0f;
-    unsigned long long wf = 1;
     bool done = false;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -969,14 +968,13 @@ __global__ void __launch_bounds__(kPlainThreads, 4) sample_plain_kernel(const Sa
         done = true;
         found = e;
         xf = x[e];
-        wf = w[e];
       }
     }
     a.tokens[row] = id0 + q * kPlainTile + lane * E + found;
     if (a.logprob) {
       RowWeights<7> r = rw;
       r.sh = 0.0f;  // xf is shifted
-      a.logprob[row] = log_share(r, xf, T, wf, total);
+      a.logprob[row] = log_share(r, xf, T, weight_of(xf), total);
     }
   }
 }
