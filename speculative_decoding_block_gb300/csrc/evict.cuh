@@ -14,7 +14,7 @@
 // are moved in batches of ascending j, which write rows below all that any
 // later batch reads: one barrier per batch is needed, between its own reads
 // and its writes.  More CTAs per SM keep more bytes in flight than reading a
-// batch ahead does (three of 512 threads with four 16-byte words each 221 us,
+// batch ahead does (three of 512 threads with four 16-byte words each 215 us,
 // two of 256 with eight words and a batch ahead 278 us for 1.1 GB: 16 requests
 // of 4096 rows cut to 1024, 8 layers, 8 heads of 128).
 #pragma once
