@@ -19,7 +19,8 @@ struct KvView {
   size_t ws_floats_o, ws_floats_ml;
 };
 KvView kv_view(const vsd_kv* kv);
-// The cache's workspace for scores [max_batch][n_q][max_tokens], allocated on the first call (not while `st` is captured).
+// The cache's workspace for scores [max_batch][n_q][max_tokens], allocated now where the cache's creation found no memory
+// (refused while `st` is captured).
 vsd_status kv_raw_scores(vsd_kv* kv, cudaStream_t st, float** out);
 
 }  // namespace vsd
