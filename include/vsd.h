@@ -521,7 +521,8 @@ vsd_status vsd_decode_attention(const vsd_model* m, vsd_kv* kv, int32_t layer, i
  * is no error) or a page of rows [0, L_b) outside the pool
  * (VSD_DEV_BAD_PAGE) leaves the request as it was: new_lens = L_b, kept -1.
  * A bit and a count per row of the cache's room have to fit in shared memory:
- * max_tokens_per_req above some 800,000 is refused (VSD_ERR_UNSUPPORTED). */
+ * max_tokens_per_req above some 800,000 is refused (VSD_ERR_UNSUPPORTED), for
+ * few requests, whose rows are split over several SMs, up to eight times that. */
 vsd_status vsd_kv_evict(vsd_kv* kv, int32_t batch, const int32_t* seq_lens_dev, int32_t* new_lens_dev,
                         float* score_dev, int32_t budget, int32_t sinks, int32_t recent, int32_t* kept_dev,
                         vsd_stream stream);

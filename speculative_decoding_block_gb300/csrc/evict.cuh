@@ -19,15 +19,15 @@
 // of 4096 rows cut to 1024, 8 layers, 8 heads of 128).
 #pragma once
 
-#include "vsd_common.cuh"
+#include "cluster_mem.cuh"
 
 namespace vsd {
 
 struct EvictArgs {
   int batch, layers, n_kv, num_pages, ppr, max_tokens, budget, sinks, recent;
   int cs;            // CTAs per (layer, request, KV head)
-  int words;         // 32-row words of a request at its longest
-  int cache;         // scores kept in shared memory, where a request has no more
+  int words;         // 32-row words of a CTA's share of a request at its longest
+  int cache;         // scores kept in shared memory, where a share has no more
   const int* lens;   // [B]
   int* new_lens;     // [B]; nullptr: written by a launch of its own (lens is the same array)
   const int* page_table;
@@ -40,13 +40,26 @@ struct EvictArgs {
 // Orderable key of a score: NaN lowest, -0 equal to +0.
 __device__ __forceinline__ uint32_t score_key(float f) { return f != f ? 0u : float_order_key(f + 0.0f); }
 
-constexpr int kEvictThreads = 512;
-constexpr int kEvictUnroll = 4;  // 16-byte words of a thread per batch
 constexpr int kEvictBins = 2048;
-constexpr int kEvictWindow = 1024;  // kept rows listed at a time
 constexpr int kEvictMaxCluster = 8;
-constexpr int evict_batch(int hd) { return kEvictThreads * kEvictUnroll / (2 * (hd / 8)); }  // rows of a CTA's batch
-inline int evict_smem_bytes(int words, int cache) { return (kEvictBins + kEvictWindow + 2 * words + cache) * 4; }
+// The three forms of the kernel.
+struct EvictWide {  // one CTA per SM at most: long batches, so that few barriers stand between the moves
+  static constexpr int threads = 512, unroll = 16, window = 4096, per_sm = 1, most_cached = 32768;
+  static constexpr bool clusters = true;
+};
+struct EvictFull {  // all SMs full
+  static constexpr int threads = 512, unroll = 4, window = 1024, per_sm = 3, most_cached = 8192;
+  static constexpr bool clusters = false;
+};
+struct EvictShort {  // many short requests: the chain of a CTA's steps is what takes the time, so many of them at once
+  static constexpr int threads = 128, unroll = 4, window = 256, per_sm = 12, most_cached = 1024;
+  static constexpr bool clusters = false;
+};
+// unroll: 16-byte words of a thread per batch; window: kept rows listed at a time, a multiple of a cluster's batch
+template <class Form>
+constexpr int evict_batch(int hd) { return Form::threads * Form::unroll / (2 * (hd / 8)); }  // rows of a CTA's batch
+template <class Form>
+int evict_smem_bytes(int words, int cache) { return ((Form::clusters ? 3 : 1) * kEvictBins + Form::window + 2 * words + cache) * 4; }
 
 // Whether request b's rows [0, L) lie in the pool (every thread of the CTA).
 __device__ __forceinline__ bool pages_ok(const int* pages, int L, int num_pages) {
@@ -60,18 +73,22 @@ __device__ __forceinline__ int evicted_len(int L, int budget, int max_tokens, bo
   return (L >= 0 && L <= max_tokens && ok) ? min(L, budget) : L;
 }
 
-template <int HD>
-__global__ void __launch_bounds__(kEvictThreads, 3) evict_kernel(const EvictArgs a) {
+template <int HD, class Form>
+__global__ void __launch_bounds__(Form::threads, Form::per_sm) evict_kernel(const EvictArgs a) {
+  constexpr int T = Form::threads, W = T / 32, U = Form::unroll, kWindow = Form::window;
+  constexpr bool CL = Form::clusters;
   constexpr int V = HD / 8;  // 16-byte words of a row
-  constexpr int RB = evict_batch(HD), W = kEvictThreads / 32, U = kEvictUnroll;
+  constexpr int RB = evict_batch<Form>(HD);
+  constexpr int E = kEvictBins / T;  // bins of a thread
+  static_assert(kWindow % (CL ? kEvictMaxCluster * RB : RB) == 0 && RB <= T && E % 4 == 0);
   extern __shared__ __align__(16) uint32_t evict_smem[];
-  uint32_t* hist = evict_smem;
-  int* win = reinterpret_cast<int*>(hist + kEvictBins);
-  uint32_t* mask = reinterpret_cast<uint32_t*>(win + kEvictWindow);  // rows that stay
-  uint32_t* count = mask + a.words;                                  // of them in front of the word (equals' bits before that)
+  uint32_t* hists = evict_smem;  // one, or one a digit where other CTAs read it
+  uint32_t* win = hists + (CL ? 3 : 1) * kEvictBins;
+  uint32_t* mask = win + kWindow;     // rows that stay, of this CTA's words
+  uint32_t* count = mask + a.words;   // of them in front of the word (equals' bits before that)
   float* cache = reinterpret_cast<float*>(count + a.words);
-  __shared__ uint32_t red[W], found[3];
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, cs = a.cs;
+  __shared__ uint32_t red[W], found[3], xch[2][kEvictMaxCluster];
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, cs = CL ? a.cs : 1;
   const int item = static_cast<int>(blockIdx.x) / cs, rank = static_cast<int>(blockIdx.x) % cs;
   const int h = item % a.n_kv, b = (item / a.n_kv) % a.batch, layer = item / a.n_kv / a.batch;
   const int L = a.lens[b];
@@ -86,11 +103,18 @@ __global__ void __launch_bounds__(kEvictThreads, 3) evict_kernel(const EvictArgs
   int* kept = a.kept ? a.kept + static_cast<size_t>(item) * a.budget : nullptr;
   if (!ok || L <= a.budget) {  // the whole cluster alike
     if (kept && rank == 0)
-      for (int64_t j = t; j < a.budget; j += kEvictThreads) kept[j] = (ok && j < L) ? static_cast<int>(j) : -1;
+      for (int64_t j = t; j < a.budget; j += T) kept[j] = (ok && j < L) ? static_cast<int>(j) : -1;
     return;
   }
   float* score = a.score ? a.score + static_cast<size_t>(item) * a.max_tokens : nullptr;  // nullptr only where nothing is chosen
   const int mid0 = a.sinks, mid1 = L - a.recent, want = a.budget - a.sinks - a.recent;
+  // this CTA's words of 32 rows, and its rows [r0, r1)
+  const int words = (L + 31) / 32, share = (words + cs - 1) / cs, wa = min(words, rank * share), nw = min(words, wa + share) - wa;
+  const int r0 = wa * 32, r1 = min(L, r0 + nw * 32);
+  auto sync_all = [&]() {
+    if (cs > 1) cluster_sync();
+    else __syncthreads();
+  };
   // sum over the threads before this one; all: of all
   auto block_scan = [&](uint32_t v, uint32_t* all) {
     uint32_t c = v;
@@ -111,34 +135,64 @@ __global__ void __launch_bounds__(kEvictThreads, 3) evict_kernel(const EvictArgs
     *all = sum;
     return pre + c - v;
   };
+  // the other ranks' `mine`, summed over the ranks before this one
+  auto ranks_before = [&](int turn, uint32_t mine) {
+    if (cs == 1) return 0u;
+    if (t < cs) st_dsmem_u32(mapa_shared(smem_u32(&xch[turn][rank]), t), mine);
+    cluster_sync();
+    uint32_t pre = 0;
+    for (int r = 0; r < rank; ++r) pre += xch[turn][r];
+    return pre;
+  };
+  for (int i = t; i < (CL ? 3 : 1) * kEvictBins; i += T) hists[i] = 0;
+  sync_all();  // and every CTA of the cluster has started
 
   // ------------------------------------------------------------------ the want-th largest key of rows [mid0, mid1)
   uint32_t thr = 0, need = 0, equals = 0;  // kept: keys above thr and the first `need` of its `equals`
-  const bool cached = score && L <= a.cache;
+  const bool cached = score && share * 32 <= a.cache;
   if (want > 0) {
     need = static_cast<uint32_t>(want);
 #pragma unroll 1
     for (int level = 0; level < 3; ++level) {
       const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11;
-      for (int i = t; i < kEvictBins; i += kEvictThreads) hist[i] = 0;
-      __syncthreads();
+      uint32_t* hist = CL ? hists + level * kEvictBins : hists;
+      if (!CL && level) {
+        for (int i = t; i < kEvictBins; i += T) hist[i] = 0;
+        __syncthreads();
+      }
 #pragma unroll 4
-      for (int i = (level == 0 ? 0 : mid0) + t; i < (level == 0 ? L : mid1); i += kEvictThreads) {
-        const float s = level && cached ? cache[i] : score[i];
-        if (!level && cached) cache[i] = s;
+      for (int i = r0 + t; i < r1; i += T) {
+        const float s = level && cached ? cache[i - r0] : score[i];
+        if (!level && cached) cache[i - r0] = s;
         const uint32_t k = score_key(s);
         if (i >= mid0 && i < mid1 && (!level || (k >> (shift + bits)) == (thr >> (shift + bits))))
           atomicAdd(&hist[kEvictBins - 1 - ((k >> shift) & ((1u << bits) - 1))], 1u);  // largest first
       }
-      __syncthreads();
-      uint32_t n[kEvictBins / kEvictThreads], sum = 0, all;
+      sync_all();
+      uint32_t n[E], sum = 0, all;
 #pragma unroll
-      for (int e = 0; e < kEvictBins / kEvictThreads; ++e) sum += n[e] = hist[t * (kEvictBins / kEvictThreads) + e];
+      for (int e = 0; e < E; e += 4) {
+        uint4 v = *reinterpret_cast<const uint4*>(hist + t * E + e);
+        if (cs > 1) {
+          v = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int r = 0; r < kEvictMaxCluster; ++r)
+            if (r < cs) {
+              const uint4 y = ld_dsmem_v4(mapa_shared(smem_u32(hist + t * E + e), r));
+              v = make_uint4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
+            }
+        }
+        n[e] = v.x;
+        n[e + 1] = v.y;
+        n[e + 2] = v.z;
+        n[e + 3] = v.w;
+        sum += v.x + v.y + v.z + v.w;
+      }
       uint32_t before = block_scan(sum, &all);
 #pragma unroll
-      for (int e = 0; e < kEvictBins / kEvictThreads; ++e) {
+      for (int e = 0; e < E; ++e) {
         if (before < need && need <= before + n[e]) {  // one thread
-          found[0] = static_cast<uint32_t>(kEvictBins - 1 - (t * (kEvictBins / kEvictThreads) + e));
+          found[0] = static_cast<uint32_t>(kEvictBins - 1 - (t * E + e));
           found[1] = need - before;
           found[2] = n[e];
         }
@@ -152,12 +206,11 @@ __global__ void __launch_bounds__(kEvictThreads, 3) evict_kernel(const EvictArgs
   }
 
   // ------------------------------------------------------------------ what stays, a bit per row
-  const int words = (L + 31) / 32;
 #pragma unroll 2
-  for (int w = warp; w < words; w += W) {
-    const int i = w * 32 + lane;
+  for (int w = warp; w < nw; w += W) {
+    const int i = r0 + w * 32 + lane;
     const bool in_mid = i >= mid0 && i < mid1;
-    const uint32_t k = want > 0 && in_mid ? score_key(cached ? cache[i] : score[i]) : 0;
+    const uint32_t k = want > 0 && in_mid ? score_key(cached ? cache[i - r0] : score[i]) : 0;
     const bool tie = want > 0 && in_mid && k == thr;
     const uint32_t ties = __ballot_sync(0xFFFFFFFFu, tie);
     const uint32_t stay = __ballot_sync(0xFFFFFFFFu, i < L && (!in_mid || (want > 0 && k > thr)));
@@ -167,12 +220,13 @@ __global__ void __launch_bounds__(kEvictThreads, 3) evict_kernel(const EvictArgs
     }
   }
   __syncthreads();
-  const int run = (words + kEvictThreads - 1) / kEvictThreads, w0 = min(words, t * run), w1 = min(words, w0 + run);
+  const int run = (nw + T - 1) / T, w0 = min(nw, t * run), w1 = min(nw, w0 + run);
   uint32_t all;
   if (equals > need) {  // the first ones only
     uint32_t n = 0;
     for (int w = w0; w < w1; ++w) n += __popc(count[w]);
     uint32_t seen = block_scan(n, &all);
+    seen += ranks_before(0, all);
     for (int w = w0; w < w1; ++w) {
       const uint32_t ties = count[w];
       uint32_t take = ties;
@@ -184,6 +238,7 @@ __global__ void __launch_bounds__(kEvictThreads, 3) evict_kernel(const EvictArgs
   uint32_t n = 0;
   for (int w = w0; w < w1; ++w) n += __popc(mask[w]);
   uint32_t before = block_scan(n, &all);
+  before += ranks_before(1, all);
   for (int w = w0; w < w1; ++w) {
     count[w] = before;
     before += __popc(mask[w]);
@@ -191,32 +246,30 @@ __global__ void __launch_bounds__(kEvictThreads, 3) evict_kernel(const EvictArgs
   __syncthreads();
 
   // ------------------------------------------------------------------ the move
-  const size_t pool_head = (static_cast<size_t>(layer) * a.num_pages * a.n_kv + h) * kPage * HD;
-  const size_t page_elems = static_cast<size_t>(a.n_kv) * kPage * HD;
+  // row i of this head, in pages of n_kv heads
+  const size_t first_page = static_cast<size_t>(layer) * a.num_pages;
   auto row_ptr = [&](__nv_bfloat16* pool, int i) {
-    return reinterpret_cast<uint4*>(pool + pool_head + pages[i / kPage] * page_elems + (i % kPage) * HD);
+    return reinterpret_cast<uint4*>(pool + ((first_page + pages[i / kPage]) * a.n_kv + h) * (kPage * HD) + (i % kPage) * HD);
   };
-  // kept rows [first, first + kEvictWindow) into the window's list
+  // kept rows [first, first + kWindow) into the list of the CTA that moves them (RB rows each in turn)
   auto list = [&](int first) {
-    for (int w = t; w < words; w += kEvictThreads) {
-      uint32_t m = mask[w];
-      int j = static_cast<int>(count[w]) - first;
-      if (j >= kEvictWindow || j + 32 <= 0) continue;
-      for (; m; m &= m - 1, ++j)
-        if (j >= 0 && j < kEvictWindow) {
-          const int i = w * 32 + __ffs(m) - 1;
-          win[j] = i;
-          if (kept && rank == 0) kept[first + j] = i;
-        }
+    for (int w = warp; w < nw; w += W) {  // a lane per row
+      const uint32_t m = mask[w];
+      const int j = static_cast<int>(count[w] + __popc(m & ((1u << lane) - 1))) - first;
+      if ((m >> lane & 1) && j >= 0 && j < kWindow) {
+        const int i = r0 + w * 32 + lane;
+        if (cs > 1) st_dsmem_u32(mapa_shared(smem_u32(&win[j]), (j / RB) % cs), static_cast<uint32_t>(i));
+        else win[j] = static_cast<uint32_t>(i);
+        if (kept) kept[first + j] = i;
+      }
     }
   };
   const int step = cs * RB;
 #pragma unroll 1
   for (int first = 0; first < a.budget; first += step) {
-    if (first % kEvictWindow == 0) {
-      __syncthreads();
-      list(first);
-      __syncthreads();
+    if (first % kWindow == 0) {
+      list(first);  // (all have read the former list: they are past the barrier of its last batch)
+      sync_all();
     }
     // this thread's words of the batch: of K and V rows, a score
     const int j0 = first + rank * RB;
@@ -225,20 +278,19 @@ __global__ void __launch_bounds__(kEvictThreads, 3) evict_kernel(const EvictArgs
     uint32_t moved = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int y = u * kEvictThreads + t, j = j0 + y / (2 * V), c = y % (2 * V);
-      const int src = j < a.budget ? win[j % kEvictWindow] : j;
+      const int y = u * T + t, j = j0 + y / (2 * V), c = y % (2 * V);
+      const int src = j < a.budget ? static_cast<int>(win[j % kWindow]) : j;
       if (src != j) {
         v[u] = row_ptr(c < V ? a.k_pool : a.v_pool, src)[c % V];
         moved |= 1u << u;
       }
     }
     const bool has_score = score && t < RB && j0 + t < a.budget;
-    if (has_score) sc = score[win[(j0 + t) % kEvictWindow]];
-    if (cs > 1) cluster_sync();
-    else __syncthreads();
+    if (has_score) sc = score[win[(j0 + t) % kWindow]];
+    sync_all();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int y = u * kEvictThreads + t, j = j0 + y / (2 * V), c = y % (2 * V);
+      const int y = u * T + t, j = j0 + y / (2 * V), c = y % (2 * V);
       if (moved >> u & 1) row_ptr(c < V ? a.k_pool : a.v_pool, j)[c % V] = v[u];
     }
     if (has_score) score[j0 + t] = sc;

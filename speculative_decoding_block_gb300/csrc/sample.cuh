@@ -30,7 +30,7 @@
 // for 32 rows of mixed settings, this 51.
 #pragma once
 
-#include "vsd_common.cuh"
+#include "cluster_mem.cuh"
 
 namespace vsd {
 
@@ -285,27 +285,6 @@ struct alignas(16) SampleShared {
   float scale[2];                       // c of the row
 };
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void st_dsmem_u64(uint32_t addr, unsigned long long v) {
-  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
-}
-__device__ __forceinline__ unsigned long long ld_dsmem_u64(uint32_t addr) {
-  unsigned long long v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t atom_add_dsmem(uint32_t addr, uint32_t v) {
-  uint32_t old;
-  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(addr), "r"(v) : "memory");
-  return old;
-}
-
-__device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
 // Adds a weight (below 2^48) to a bin; 2^16 weights fit.
 __device__ __forceinline__ void add_mass(uint32_t (*hist)[kSampleBins], int bin, unsigned long long w) {
   const uint32_t low = static_cast<uint32_t>(w), high = static_cast<uint32_t>(w >> 32);

@@ -67,20 +67,29 @@ vsd_status launch_decode(const KvView& c, DecodeArgs& a, cudaStream_t st) {
   return VSD_OK;
 }
 
+template <int HD, class Form>
+vsd_status launch_evict_as(const KvView& c, EvictArgs& a, int64_t items, cudaStream_t st) {
+  a.words = ceil_div_h(ceil_div_h(c.max_tokens, 32), a.cs);
+  a.cache = a.words * 32 <= Form::most_cached ? a.words * 32 : 0;
+  const int smem = evict_smem_bytes<Form>(a.words, a.cache);
+  if (smem > 227 * 1024 - 1024) return fail(VSD_ERR_UNSUPPORTED, "max_tokens_per_req %d is too long for an eviction", c.max_tokens);
+  CK(ensure_smem_opt_in(reinterpret_cast<const void*>(evict_kernel<HD, Form>), smem));
+  CK(launch_ex_cluster(evict_kernel<HD, Form>, dim3(static_cast<unsigned>(items * a.cs)), dim3(Form::threads), smem, a.cs, st, false, a));
+  return VSD_OK;
+}
+
 template <int HD>
 vsd_status launch_evict(const KvView& c, EvictArgs& a, cudaStream_t st) {
   const int64_t items = static_cast<int64_t>(c.layers) * a.batch * c.n_kv;
-  // one CTA each; where they leave SMs idle and have many batches to move, a cluster (its barrier per batch costs what a
-  // CTA's does not)
   a.cs = 1;
-  while (a.cs < kEvictMaxCluster && items * a.cs * 2 <= c.sms && a.budget > 8 * a.cs * evict_batch(HD)) a.cs *= 2;
-  a.words = ceil_div_h(c.max_tokens, 32);
-  a.cache = c.max_tokens <= 8192 ? c.max_tokens : 0;
-  const int smem = evict_smem_bytes(a.words, a.cache);
-  if (smem > 227 * 1024 - 1024) return fail(VSD_ERR_UNSUPPORTED, "max_tokens_per_req %d is too long for an eviction", c.max_tokens);
-  CK(ensure_smem_opt_in(reinterpret_cast<const void*>(evict_kernel<HD>), smem));
-  CK(launch_ex_cluster(evict_kernel<HD>, dim3(static_cast<unsigned>(items * a.cs)), dim3(kEvictThreads), smem, a.cs, st, false, a));
-  return VSD_OK;
+  if (items <= c.sms) {
+    // one CTA each, or a cluster where there are many batches to move (its barrier per batch costs what a CTA's does not)
+    while (a.cs < kEvictMaxCluster && items * a.cs * 2 <= c.sms && (a.budget > a.cs * evict_batch<EvictWide>(HD) || c.max_tokens > a.cs * 4096))
+      a.cs *= 2;
+    return launch_evict_as<HD, EvictWide>(c, a, items, st);
+  }
+  if (c.max_tokens <= EvictShort::most_cached && a.budget * HD <= 16384 && items > EvictFull::per_sm * c.sms) return launch_evict_as<HD, EvictShort>(c, a, items, st);
+  return launch_evict_as<HD, EvictFull>(c, a, items, st);
 }
 
 vsd_status launch_sample(SampleRowArgs& a, cudaStream_t st) {
@@ -201,7 +210,7 @@ vsd_status vsd_kv_evict(vsd_kv* kv, int32_t batch, const int32_t* seq_lens, int3
   if (s) return s;
   if ((s = c.hd == 64 ? launch_evict<64>(c, a, st) : launch_evict<128>(c, a, st))) return s;
   if (!a.new_lens) {
-    evict_lens_kernel<<<batch, kEvictThreads, 0, st>>>(a, new_lens);
+    evict_lens_kernel<<<batch, 256, 0, st>>>(a, new_lens);
     CK(cudaGetLastError());
   }
   return VSD_OK;

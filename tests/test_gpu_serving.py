@@ -461,6 +461,47 @@ def test_eviction_of_a_long_request(L):
     check_eviction(c, scores_for(c, "ties"), L // 3, 4, 100)
 
 
+def filled_cache(B, layers, n_q, n_kv, hd, lens, room):
+    """A cache over shuffled pages whose pools hold random values everywhere."""
+    c = Cache.__new__(Cache)
+    c.B, c.layers, c.n_q, c.n_kv, c.hd, c.lens, c.max_tokens = B, layers, n_q, n_kv, hd, list(lens), room
+    c.model = tiny_model(B, layers, n_q, n_kv, hd, 131072)
+    ppr = -(-room // 16)
+    c.kv = B.vsd_kv_create(c.model, len(lens), room, 16, len(lens) * ppr + 2)
+    c.table = gen._rng("fill", room).permutation(c.kv.num_pages)[: len(lens) * ppr].astype(np.int32).reshape(len(lens), ppr)
+    B.vsd_kv_set_page_table(c.kv, torch.tensor(c.table.reshape(-1), device="cuda"))
+    c.k_pool, c.v_pool = B.vsd_kv_pools(c.kv)
+    g = torch.Generator("cuda").manual_seed(room)
+    c.k_pool.normal_(generator=g)
+    c.v_pool.normal_(generator=g)
+    c.seq = torch.tensor(c.lens, dtype=torch.int32, device="cuda")
+    return c
+
+
+@pytest.mark.parametrize("kind", ["random", "ties", "equal", "odd"])
+@pytest.mark.parametrize("heads,lens,room,budget", [
+    ((4, 2, 128), [9000, 4097, 5003, -1, 8999, 33], 9000, 4097),     # clusters of CTAs, budgets past one list of them
+    ((4, 2, 64), [9000, 4097, 5003, 0], 9000, 8998),
+    ((4, 1, 128), [20011], 20011, 700),
+    ((4, 4, 64), [33001] + [700] * 19, 33001, 640),                  # a CTA a head, its scores too many for shared memory
+    ((8, 8, 64), [1100, 640, 601, 599] * 5, 1100, 600),              # more heads than SMs
+    ((8, 8, 128), [8300, 9000, 77] + [300] * 17, 9000, 256),         # the same, scores not kept
+])
+def test_eviction_forms(kind, heads, lens, room, budget):
+    """Few, long requests split over clusters; heads for every SM; scores that fit in shared memory and not."""
+    B = require_gpu()
+    c = filled_cache(B, 1, *heads, lens, room)
+    check_eviction(c, scores_for(c, kind), budget, 4, 60)
+
+
+@pytest.mark.parametrize("kind", ["random", "ties", "odd"])
+@pytest.mark.parametrize("hd,budget", [(64, 200), (128, 100), (128, 1), (64, 17)])
+def test_eviction_of_many_short_requests(kind, hd, budget):
+    B = require_gpu()
+    c = filled_cache(B, 2, 4, 4, hd, [300, 101, 200, 99, 0, -1, 257, 18, 2, 33] * 6, 300)
+    check_eviction(c, scores_for(c, kind), budget, budget // 8, budget // 3)
+
+
 def test_eviction_rejects_bad_requests_and_spares_the_others():
     B = require_gpu()
     c = Cache(B, 1, 4, 2, 64, [100, 100, 100], 128, fill=0.0, tag="evbad")
@@ -785,11 +826,19 @@ def test_decode_attention_follows_a_verify_step():
 
 def test_eviction_refuses_a_room_beyond_its_bitmap():
     B = require_gpu()
-    kv = B.vsd_kv_create(tiny_model(B, 1, 1, 1, 64, 1_000_000), 1, 950_000)
-    seq = torch.tensor([10], dtype=torch.int32, device="cuda")
+    room, n_b = 950_000, 80  # more requests than half the SMs: a CTA each
+    kv = B.vsd_kv_create(tiny_model(B, 1, 1, 1, 64, 1_000_000), n_b, room, 16, 64)
+    seq = torch.full((n_b,), 10, dtype=torch.int32, device="cuda")
+    score = torch.zeros((1, n_b, 1, room), device="cuda")
+    new = torch.zeros_like(seq)
     with pytest.raises(B.VsdError) as e:
-        B.vsd_kv_evict(kv, 1, seq, torch.zeros_like(seq), torch.zeros((1, 1, 1, 950_000), device="cuda"), 4)
+        B.vsd_kv_evict(kv, n_b, seq, new, score, 4)
     assert e.value.status == B.VSD_ERR_UNSUPPORTED
+    # one request of that room is split over a cluster
+    B.vsd_kv_set_page_table(kv, torch.zeros(n_b * (room // 16), dtype=torch.int32, device="cuda"))
+    B.vsd_kv_evict(kv, 1, seq, new, score, 4)
+    torch.cuda.synchronize()
+    assert new[0] == 4 and not new[1:].any() and B.vsd_get_device_status(kv) == 0
 
 
 def test_eviction_with_a_budget_of_the_whole_type():
