@@ -59,7 +59,7 @@ struct EvictShort {  // many short requests: the chain of a CTA's steps is what 
 template <class Form>
 constexpr int evict_batch(int hd) { return Form::threads * Form::unroll / (2 * (hd / 8)); }  // rows of a CTA's batch
 template <class Form>
-int evict_smem_bytes(int words, int cache) { return ((Form::clusters ? 3 : 1) * kEvictBins + Form::window + 2 * words + cache) * 4; }
+int evict_smem_bytes(int words, int cache) { return ((Form::clusters ? 3 : 1) * kEvictBins + 2 * Form::window + 2 * words + cache) * 4; }
 
 // Whether request b's rows [0, L) lie in the pool (every thread of the CTA).
 __device__ __forceinline__ bool pages_ok(const int* pages, int L, int num_pages) {
@@ -84,7 +84,8 @@ __global__ void __launch_bounds__(Form::threads, Form::per_sm) evict_kernel(cons
   extern __shared__ __align__(16) uint32_t evict_smem[];
   uint32_t* hists = evict_smem;  // one, or one a digit where other CTAs read it
   uint32_t* win = hists + (CL ? 3 : 1) * kEvictBins;
-  uint32_t* mask = win + kWindow;     // rows that stay, of this CTA's words
+  uint32_t* place = win + kWindow;    // and where they lie: 16 * page + row in it
+  uint32_t* mask = place + kWindow;   // rows that stay, of this CTA's words
   uint32_t* count = mask + a.words;   // of them in front of the word (equals' bits before that)
   float* cache = reinterpret_cast<float*>(count + a.words);
   __shared__ uint32_t red[W], found[3], xch[2][kEvictMaxCluster];
@@ -246,10 +247,10 @@ __global__ void __launch_bounds__(Form::threads, Form::per_sm) evict_kernel(cons
   __syncthreads();
 
   // ------------------------------------------------------------------ the move
-  // row i of this head, in pages of n_kv heads
+  // a row of this head by its place, in pages of n_kv heads
   const size_t first_page = static_cast<size_t>(layer) * a.num_pages;
-  auto row_ptr = [&](__nv_bfloat16* pool, int i) {
-    return reinterpret_cast<uint4*>(pool + ((first_page + pages[i / kPage]) * a.n_kv + h) * (kPage * HD) + (i % kPage) * HD);
+  auto row_ptr = [&](__nv_bfloat16* pool, uint32_t at) {
+    return reinterpret_cast<uint4*>(pool + ((first_page + at / kPage) * a.n_kv + h) * (kPage * HD) + (at % kPage) * HD);
   };
   // kept rows [first, first + kWindow) into the list of the CTA that moves them (RB rows each in turn)
   auto list = [&](int first) {
@@ -258,8 +259,14 @@ __global__ void __launch_bounds__(Form::threads, Form::per_sm) evict_kernel(cons
       const int j = static_cast<int>(count[w] + __popc(m & ((1u << lane) - 1))) - first;
       if ((m >> lane & 1) && j >= 0 && j < kWindow) {
         const int i = r0 + w * 32 + lane;
-        if (cs > 1) st_dsmem_u32(mapa_shared(smem_u32(&win[j]), (j / RB) % cs), static_cast<uint32_t>(i));
-        else win[j] = static_cast<uint32_t>(i);
+        const uint32_t at = static_cast<uint32_t>(pages[i / kPage]) * kPage + i % kPage;
+        if (cs > 1) {
+          st_dsmem_u32(mapa_shared(smem_u32(&win[j]), (j / RB) % cs), static_cast<uint32_t>(i));
+          st_dsmem_u32(mapa_shared(smem_u32(&place[j]), (j / RB) % cs), at);
+        } else {
+          win[j] = static_cast<uint32_t>(i);
+          place[j] = at;
+        }
         if (kept) kept[first + j] = i;
       }
     }
@@ -279,9 +286,8 @@ __global__ void __launch_bounds__(Form::threads, Form::per_sm) evict_kernel(cons
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int y = u * T + t, j = j0 + y / (2 * V), c = y % (2 * V);
-      const int src = j < a.budget ? static_cast<int>(win[j % kWindow]) : j;
-      if (src != j) {
-        v[u] = row_ptr(c < V ? a.k_pool : a.v_pool, src)[c % V];
+      if (j < a.budget && static_cast<int>(win[j % kWindow]) != j) {
+        v[u] = row_ptr(c < V ? a.k_pool : a.v_pool, place[j % kWindow])[c % V];
         moved |= 1u << u;
       }
     }
@@ -291,7 +297,7 @@ __global__ void __launch_bounds__(Form::threads, Form::per_sm) evict_kernel(cons
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int y = u * T + t, j = j0 + y / (2 * V), c = y % (2 * V);
-      if (moved >> u & 1) row_ptr(c < V ? a.k_pool : a.v_pool, j)[c % V] = v[u];
+      if (moved >> u & 1) row_ptr(c < V ? a.k_pool : a.v_pool, static_cast<uint32_t>(pages[j / kPage]) * kPage + j % kPage)[c % V] = v[u];
     }
     if (has_score) score[j0 + t] = sc;
   }
