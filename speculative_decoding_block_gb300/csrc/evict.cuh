@@ -6,17 +6,22 @@
 // lowest rows; NaN counts as below every number.  Kept rows keep their order
 // and move to rows [0, budget) of the same pages.
 //
-// Bound by the bytes of the kept rows, read and written once.  One CTA (or,
-// where there are few and long ones, a cluster) per (layer, request, KV head):
-// the smallest kept score by three digits of 11, 11 and 10 bits of its ordered
-// key; a bit per row for what stays, with a running count per 32 rows; then the
-// move.  Moving in place: kept row number j comes from row r_j >= j, and rows
-// are moved in batches of ascending j, which write rows below all that any
-// later batch reads: one barrier per batch is needed, between its own reads
-// and its writes.  More CTAs per SM keep more bytes in flight than reading a
-// batch ahead does (three of 512 threads with four 16-byte words each 215 us,
-// two of 256 with eight words and a batch ahead 278 us for 1.1 GB: 16 requests
-// of 4096 rows cut to 1024, 8 layers, 8 heads of 128).
+// Bound by the bytes of the kept rows, read and written once.  A CTA (or,
+// where heads are few, a cluster, each CTA with an equal share of the rows) per
+// (layer, request, KV head): the smallest kept score by three digits of 11, 11
+// and 10 bits of its ordered key, the CTAs' counts added up through distributed
+// shared memory; a bit per row for what stays, with a running count per 32
+// rows; then the move.  Moving in place: kept row number j comes from row
+// r_j >= j, and rows are moved in batches of ascending j, which write rows below
+// all that any later batch reads: one barrier per batch is needed, between its
+// own reads and its writes.
+//
+// Measured on fresh caches: 16 requests of 4096 rows cut to 1024, 8 layers, 8
+// heads of 128, 203 us for 1.1 GB (79 % of the copy bandwidth; three CTAs of
+// 512 threads per SM keep more bytes in flight than two of 256 that read a
+// batch ahead, 278 us); 24 layers of one request of 2048 rows cut to 512, 2
+// heads of 64, 18 us; 8 heads of 100,000 rows cut to 20,000 143 us (334 with
+// every CTA counting all rows).
 #pragma once
 
 #include "cluster_mem.cuh"
@@ -84,7 +89,7 @@ __global__ void __launch_bounds__(Form::threads, Form::per_sm) evict_kernel(cons
   extern __shared__ __align__(16) uint32_t evict_smem[];
   uint32_t* hists = evict_smem;  // one, or one a digit where other CTAs read it
   uint32_t* win = hists + (CL ? 3 : 1) * kEvictBins;
-  uint32_t* place = win + kWindow;    // and where they lie: 16 * page + row in it
+  uint32_t* place = win + kWindow;    // and where they lie in the layer's pool
   uint32_t* mask = place + kWindow;   // rows that stay, of this CTA's words
   uint32_t* count = mask + a.words;   // of them in front of the word (equals' bits before that)
   float* cache = reinterpret_cast<float*>(count + a.words);
@@ -247,10 +252,11 @@ __global__ void __launch_bounds__(Form::threads, Form::per_sm) evict_kernel(cons
   __syncthreads();
 
   // ------------------------------------------------------------------ the move
-  // a row of this head by its place, in pages of n_kv heads
-  const size_t first_page = static_cast<size_t>(layer) * a.num_pages;
-  auto row_ptr = [&](__nv_bfloat16* pool, uint32_t at) {
-    return reinterpret_cast<uint4*>(pool + ((first_page + at / kPage) * a.n_kv + h) * (kPage * HD) + (at % kPage) * HD);
+  // rows of the layer, by their place in it (32 bits: 2^32 rows are more than the device holds)
+  const size_t layer_elems = static_cast<size_t>(layer) * a.num_pages * a.n_kv * (kPage * HD);
+  auto place_of = [&](int i) { return (static_cast<uint32_t>(pages[i / kPage]) * a.n_kv + h) * kPage + i % kPage; };
+  auto row_ptr = [&](int c, uint32_t at) {  // word c of a place's K, then V
+    return reinterpret_cast<uint4*>((c < V ? a.k_pool : a.v_pool) + layer_elems + static_cast<size_t>(at) * HD) + c % V;
   };
   // kept rows [first, first + kWindow) into the list of the CTA that moves them (RB rows each in turn)
   auto list = [&](int first) {
@@ -259,7 +265,7 @@ __global__ void __launch_bounds__(Form::threads, Form::per_sm) evict_kernel(cons
       const int j = static_cast<int>(count[w] + __popc(m & ((1u << lane) - 1))) - first;
       if ((m >> lane & 1) && j >= 0 && j < kWindow) {
         const int i = r0 + w * 32 + lane;
-        const uint32_t at = static_cast<uint32_t>(pages[i / kPage]) * kPage + i % kPage;
+        const uint32_t at = place_of(i);
         if (cs > 1) {
           st_dsmem_u32(mapa_shared(smem_u32(&win[j]), (j / RB) % cs), static_cast<uint32_t>(i));
           st_dsmem_u32(mapa_shared(smem_u32(&place[j]), (j / RB) % cs), at);
@@ -287,7 +293,7 @@ __global__ void __launch_bounds__(Form::threads, Form::per_sm) evict_kernel(cons
     for (int u = 0; u < U; ++u) {
       const int y = u * T + t, j = j0 + y / (2 * V), c = y % (2 * V);
       if (j < a.budget && static_cast<int>(win[j % kWindow]) != j) {
-        v[u] = row_ptr(c < V ? a.k_pool : a.v_pool, place[j % kWindow])[c % V];
+        v[u] = *row_ptr(c, place[j % kWindow]);
         moved |= 1u << u;
       }
     }
@@ -297,7 +303,7 @@ __global__ void __launch_bounds__(Form::threads, Form::per_sm) evict_kernel(cons
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int y = u * T + t, j = j0 + y / (2 * V), c = y % (2 * V);
-      if (moved >> u & 1) row_ptr(c < V ? a.k_pool : a.v_pool, static_cast<uint32_t>(pages[j / kPage]) * kPage + j % kPage)[c % V] = v[u];
+      if (moved >> u & 1) *row_ptr(c, place_of(j)) = v[u];
     }
     if (has_score) score[j0 + t] = sc;
   }
