@@ -57,7 +57,8 @@ struct EvictFull {  // all SMs full
   static constexpr bool clusters = false;
 };
 struct EvictShort {  // many short requests: the chain of a CTA's steps is what takes the time, so many of them at once
-  static constexpr int threads = 128, unroll = 4, window = 256, per_sm = 12, most_cached = 1024;
+  // (eight a SM; twelve spilled and took 57 us where these take 52)
+  static constexpr int threads = 128, unroll = 8, window = 256, per_sm = 8, most_cached = 1024;
   static constexpr bool clusters = false;
 };
 // unroll: 16-byte words of a thread per batch; window: kept rows listed at a time, a multiple of a cluster's batch

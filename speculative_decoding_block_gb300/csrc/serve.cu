@@ -83,8 +83,8 @@ vsd_status launch_evict(const KvView& c, EvictArgs& a, cudaStream_t st) {
   const int64_t items = static_cast<int64_t>(c.layers) * a.batch * c.n_kv;
   // Times in us on fresh caches.  Wide against full: 48 heads of 2048 rows of 64 cut to 512 18 against 22, 152 of them 20.5
   // against 26, 30 of 13,381 rows of 128 cut to 3607 in clusters of 4 51 against 143.  Short against full: 2560 heads of 82-147
-  // rows of 128 cut to 66 57 against 73, 2200 of up to 105 to 35 32 against 43; but 2048 of 500 to 250 112 against 104 (there
-  // the bytes count), and 1536 of 1000 rows of 64 to 100 51 either way.
+  // rows of 128 cut to 66 52 against 73, 2200 of up to 105 to 35 30 against 43, 1536 of 1000 rows of 64 to 100 46 against 51; but
+  // 2048 of 500 rows of 128 to 250 106 against 101, and 1024 of 4096 to 1024 245 against 203: there the bytes count.
   a.cs = 1;
   if (items <= c.sms) {
     // a CTA each, or a cluster where there are batches to move or rows to count for several, and SMs for them
