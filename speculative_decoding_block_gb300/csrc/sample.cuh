@@ -271,6 +271,7 @@ constexpr int kSampleThreads = 1024;
 constexpr int kSampleBins = 2048;
 constexpr int kSampleMaxCluster = 8;
 constexpr int kSampleList = 1024;  // an entry a thread
+constexpr int kSampleFew = 256;    // entries that are compared with all others
 
 // In front of the row's slice.
 struct alignas(16) SampleShared {
@@ -312,7 +313,9 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_logits_kernel(const 
   const int id0 = min(a.vocab, rank * a.per), n = min(a.vocab, id0 + a.per) - id0;
   const float* src = a.logits + row * a.ld + id0;
   const float T = a.temperature ? a.temperature[row] : 1.0f;
-  if (t == 0) sh.n_list = 0;
+  const int top_k = a.top_k ? a.top_k[row] : 0;
+  const float top_p = a.top_p ? a.top_p[row] : 1.0f, min_p = a.min_p ? a.min_p[row] : 0.0f;
+  if (t == 0) sh.n_list = sh.members = 0;
   if (cs > 1) cluster_arrive();  // the others' memory is touched once all have started
   const float2* tab = sh.tab + lane;
   const float2 power = kPow128[(t >> 5) * 4];
@@ -429,8 +432,6 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_logits_kernel(const 
   const RowWeights<5> rw = row_weights<5>(mx, sh.scale[0], sh.scale[1]);
   sh.tab[t] = row_power(rw, power);
   __syncthreads();
-  const int top_k = a.top_k ? a.top_k[row] : 0;
-  const float top_p = a.top_p ? a.top_p[row] : 1.0f, min_p = a.min_p ? a.min_p[row] : 0.0f;
   bool cut_k = top_k > 0 && top_k < a.vocab, cut_p = top_p < 1.0f;
   const unsigned long long floor_w = max(1ull, share_of(row_weight(rw, mx, tab), min_p));
   // kept: key > thr, and the first `ties` ids of key == thr, of which there are `equals`
@@ -477,7 +478,9 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_logits_kernel(const 
     }
     unsigned long long v[3], pre[3];
     v[0] = block_scan(val_s, &before);
-    v[1] = block_scan(cnt_s, &cnt_b);
+    v[1] = v[0];
+    cnt_b = before;
+    if (!cut_k) v[1] = block_scan(cnt_s, &cnt_b);
     v[2] = 0;
     exchange(v, pre);
     before += pre[0];
@@ -503,22 +506,23 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_logits_kernel(const 
       const int first = complete ? 0 : last;
       if (complete || sh.found[2] <= kSampleList) {
         if (!complete) goal = sh.found[3];
+        // into a list of the CTA's own, then, with one reservation, into rank 0's
 #pragma unroll 4
         for (int i0 = 0; i0 < n; i0 += kSampleThreads) {
           const int i = i0 + t;
           const float x = i < n ? xs[i] : -INFINITY;
           const int b = static_cast<int>(place(x));
-          const bool in = b >= first && b <= last && x > -INFINITY;
-          const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
-          if (who) {
-            uint32_t at = 0;
-            if (lane == __ffs(who) - 1) at = atom_add_dsmem(mapa_shared(smem_u32(&sh.n_list), 0), __popc(who));
-            at = __shfl_sync(0xFFFFFFFFu, at, __ffs(who) - 1) + __popc(who & ((1u << lane) - 1));
-            if (in && at < kSampleList)
-              st_dsmem_u64(mapa_shared(smem_u32(&sh.list[at]), 0),
-                           (static_cast<unsigned long long>(logit_key(x)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id0 + i)));
+          if (b >= first && b <= last && x > -INFINITY) {
+            const uint32_t at = atomicAdd(&sh.members, 1u);
+            if (at < kSampleList) sh.ord[at] = (static_cast<unsigned long long>(logit_key(x)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id0 + i));
           }
         }
+        __syncthreads();
+        const int own = min(static_cast<int>(sh.members), kSampleList);
+        if (t == 0 && own) sh.red[0] = atom_add_dsmem(mapa_shared(smem_u32(&sh.n_list), 0), static_cast<uint32_t>(own));
+        __syncthreads();
+        if (t < own && static_cast<int>(sh.red[0]) + t < kSampleList)
+          st_dsmem_u64(mapa_shared(smem_u32(&sh.list[static_cast<int>(sh.red[0]) + t]), 0), sh.ord[t]);
         sync_all();
         if (complete && rank != 0) return;
         if (rank == 0) {
@@ -529,6 +533,43 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_logits_kernel(const 
           const unsigned long long w = t < N ? row_weight(rw, x, tab) : 0;
           const float fine = static_cast<float>(kSampleList) / static_cast<float>(last - first + 1);
           const int bin = t < N ? max(0, min(kSampleList - 1, static_cast<int>((place(x) - static_cast<float>(first)) * fine))) : kSampleList - 1;
+          if (complete && N <= kSampleFew) {
+            // each entry by all others at once: its rank and the mass before it in falling order, then, of those kept, by id
+            const int sub = N <= 32 ? 5 : N <= 64 ? 4 : N <= 128 ? 3 : 2, e = t >> sub, part = t & ((1 << sub) - 1);
+            sh.vals[t] = w;
+            __syncthreads();
+            const unsigned long long me = e < N ? sh.list[e] : 0, mass = e < N ? sh.vals[e] : 0;
+            unsigned long long ahead = 0;
+            uint32_t rank_of = 0;
+            if (e < N)
+              for (int j = part; j < N; j += 1 << sub)
+                if (sh.list[j] > me) {
+                  ++rank_of;
+                  ahead += sh.vals[j];
+                }
+            auto add_parts = [&](unsigned long long v) {
+              for (int o = 1; o < 1 << sub; o <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+              return v;
+            };
+            ahead = add_parts(ahead);
+            const int before_me = static_cast<int>(add_parts(rank_of));  // (every lane takes part)
+            bool in = e < N && (!cut_k || before_me < top_k);
+            if (cut_k && cut_p) goal = max(1ull, share_of(block_scan(in && part == 0 ? mass : 0, &before), top_p));
+            if (cut_p) in = in && ahead < goal;
+            const unsigned long long kw = in && mass >= floor_w ? mass : 0;
+            if (part == 0) sh.ord[e] = kw;
+            const unsigned long long total = block_scan(part == 0 ? kw : 0, &before), to = max(1ull, share_of(total, a.u[row]));
+            unsigned long long sum = 0;
+            if (e < N)
+              for (int j = part; j < N; j += 1 << sub)
+                if (static_cast<uint32_t>(sh.list[j]) > static_cast<uint32_t>(me)) sum += sh.ord[j];  // a lower id
+            sum = add_parts(sum);
+            if (part == 0 && kw && sum < to && to <= sum + kw) {
+              a.tokens[row] = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(me));
+              if (a.logprob) a.logprob[row] = log_share(rw, key_logit(static_cast<uint32_t>(me >> 32)), T, kw, total);
+            }
+            return;
+          }
           bool keep = t < N;
           // Where the values v, in the order of falling `ord` (bins ascending), reach the goal: the border bin; an entry in it
           // gets what comes before it there, and the bin's part of the goal.
