@@ -443,19 +443,35 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_logits_kernel(const 
     // bins of equal widths below the maximum, the last for all the rest: for counts of 1/64, for masses of 1/51.2 octave, so
     // that 40 octaves are covered
     const float per_unit = cut_k ? 64.0f : 1.6f * rw.ch;
+    // (rounded by an addition: a conversion takes eight issue slots)
     auto place = [&](float x) { return fminf((mx - fmaxf(x, -3.0e38f)) * per_unit, static_cast<float>(kSampleBins - 1)); };
+    constexpr float kBinMagic = 8388608.0f;  // 2^23
+    auto bin_bits = [&](float x) { return place(x) + kBinMagic; };
     for (int i = t; i < 4 * kSampleBins; i += kSampleThreads) sh.hist[0][i] = 0;
     __syncthreads();
     unsigned long long before;
+    // four tokens' chains side by side
+    if (cut_k) {
+#pragma unroll 1
+      for (int i0 = t; i0 < n; i0 += 4 * kSampleThreads) {
+        float x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = i0 + u * kSampleThreads < n ? xs[i0 + u * kSampleThreads] : -INFINITY;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int b = __float_as_int(bin_bits(x[u])) & (kSampleBins - 1);
+          if (b < kSampleBins - 1) atomicAdd(&sh.hist[3][b], 1u);
+        }
+      }
+    } else {
 #pragma unroll 4
-    for (int i = t; i < n; i += kSampleThreads) {
-      const float x = xs[i];
-      const int b = static_cast<int>(place(x));
-      if (cut_k) {
-        if (b < kSampleBins - 1) atomicAdd(&sh.hist[3][b], 1u);
-      } else if (x > -INFINITY) {  // (also not NaN)
-        atomicAdd(&sh.hist[3][b], 1u);
-        add_mass(sh.hist, b, row_weight(rw, x, tab));
+      for (int i = t; i < n; i += kSampleThreads) {
+        const float x = xs[i];
+        if (x > -INFINITY) {  // (also not NaN)
+          const int b = __float_as_int(bin_bits(x)) & (kSampleBins - 1);
+          atomicAdd(&sh.hist[3][b], 1u);
+          add_mass(sh.hist, b, row_weight(rw, x, tab));
+        }
       }
     }
     sync_all();
@@ -507,14 +523,26 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_logits_kernel(const 
       if (complete || sh.found[2] <= kSampleList) {
         if (!complete) goal = sh.found[3];
         // into a list of the CTA's own, then, with one reservation, into rank 0's
-#pragma unroll 4
-        for (int i0 = 0; i0 < n; i0 += kSampleThreads) {
-          const int i = i0 + t;
-          const float x = i < n ? xs[i] : -INFINITY;
-          const int b = static_cast<int>(place(x));
-          if (b >= first && b <= last && x > -INFINITY) {
-            const uint32_t at = atomicAdd(&sh.members, 1u);
-            if (at < kSampleList) sh.ord[at] = (static_cast<unsigned long long>(logit_key(x)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id0 + i));
+        const float from = static_cast<float>(first) + kBinMagic, upto = static_cast<float>(last) + kBinMagic;
+#pragma unroll 1
+        for (int i0 = t; i0 < n; i0 += 4 * kSampleThreads) {
+          float x[4];
+          bool in[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) x[u] = i0 + u * kSampleThreads < n ? xs[i0 + u * kSampleThreads] : -INFINITY;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float b = bin_bits(x[u]);
+            in[u] = b >= from && b <= upto && x[u] > -INFINITY;
+          }
+          if (in[0] || in[1] || in[2] || in[3]) {  // seldom
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (in[u]) {
+                const uint32_t at = atomicAdd(&sh.members, 1u);
+                if (at < kSampleList)
+                  sh.ord[at] = (static_cast<unsigned long long>(logit_key(x[u])) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id0 + i0 + u * kSampleThreads));
+              }
           }
         }
         __syncthreads();
@@ -532,7 +560,7 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_logits_kernel(const 
           const float x = key_logit(static_cast<uint32_t>(ent >> 32));
           const unsigned long long w = t < N ? row_weight(rw, x, tab) : 0;
           const float fine = static_cast<float>(kSampleList) / static_cast<float>(last - first + 1);
-          const int bin = t < N ? max(0, min(kSampleList - 1, static_cast<int>((place(x) - static_cast<float>(first)) * fine))) : kSampleList - 1;
+          const int bin = t < N ? max(0, min(kSampleList - 1, static_cast<int>((place(x) - static_cast<float>(first) + 0.5f) * fine))) : kSampleList - 1;
           if (complete && N <= kSampleFew) {
             // each entry by all others at once: its rank and the mass before it in falling order, then, of those kept, by id
             const int sub = N <= 32 ? 5 : N <= 64 ? 4 : N <= 128 ? 3 : 2, e = t >> sub, part = t & ((1 << sub) - 1);
