@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_logits_kernel(const 
     // that 40 octaves are covered
     const float per_unit = cut_k ? 64.0f : 1.6f * rw.ch;
     // (rounded by an addition: a conversion takes eight issue slots)
-    auto place = [&](float x) { return fminf((mx - fmaxf(x, -3.0e38f)) * per_unit, static_cast<float>(kSampleBins - 1)); };
+    auto place = [&](float x) { return fminf((mx - x) * per_unit, static_cast<float>(kSampleBins - 1)); };  // (NaN: the last bin)
     constexpr float kBinMagic = 8388608.0f;  // 2^23
     auto bin_bits = [&](float x) { return place(x) + kBinMagic; };
     for (int i = t; i < 4 * kSampleBins; i += kSampleThreads) sh.hist[0][i] = 0;
@@ -452,17 +452,20 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_logits_kernel(const 
     unsigned long long before;
     // four tokens' chains side by side
     if (cut_k) {
+      auto tally = [&](float x) {
+        const int b = __float_as_int(bin_bits(x)) & (kSampleBins - 1);
+        if (b < kSampleBins - 1) atomicAdd(&sh.hist[3][b], 1u);
+      };
+      int i = t;
 #pragma unroll 1
-      for (int i0 = t; i0 < n; i0 += 4 * kSampleThreads) {
+      for (; i + 3 * kSampleThreads < n; i += 4 * kSampleThreads) {
         float x[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = i0 + u * kSampleThreads < n ? xs[i0 + u * kSampleThreads] : -INFINITY;
+        for (int u = 0; u < 4; ++u) x[u] = xs[i + u * kSampleThreads];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int b = __float_as_int(bin_bits(x[u])) & (kSampleBins - 1);
-          if (b < kSampleBins - 1) atomicAdd(&sh.hist[3][b], 1u);
-        }
+        for (int u = 0; u < 4; ++u) tally(x[u]);
       }
+      for (; i < n; i += kSampleThreads) tally(xs[i]);
     } else {
 #pragma unroll 4
       for (int i = t; i < n; i += kSampleThreads) {
@@ -524,27 +527,32 @@ __global__ void __launch_bounds__(kSampleThreads, 1) sample_logits_kernel(const 
         if (!complete) goal = sh.found[3];
         // into a list of the CTA's own, then, with one reservation, into rank 0's
         const float from = static_cast<float>(first) + kBinMagic, upto = static_cast<float>(last) + kBinMagic;
+        auto take = [&](float x, int i) {
+          const float b = bin_bits(x);
+          if (b >= from && b <= upto && x > -INFINITY) {
+            const uint32_t at = atomicAdd(&sh.members, 1u);
+            if (at < kSampleList) sh.ord[at] = (static_cast<unsigned long long>(logit_key(x)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id0 + i));
+          }
+        };
+        // a logit well below the last bin, or above the first one, is told by one comparison: the bins' borders are off by
+        // roundings of their own size and of the maximum's, 2^-21 of both is more
+        const float lo_at = mx - (static_cast<float>(last) + 0.5f) / per_unit, hi_at = mx - (static_cast<float>(first) - 0.5f) / per_unit;
+        const float lo_x = lo_at - 0x1p-21f * (fabsf(mx) + (mx - lo_at)), hi_x = first ? hi_at + 0x1p-21f * (fabsf(mx) + (mx - hi_at)) : INFINITY;
+        int i0 = t;
 #pragma unroll 1
-        for (int i0 = t; i0 < n; i0 += 4 * kSampleThreads) {
+        for (; i0 + 3 * kSampleThreads < n; i0 += 4 * kSampleThreads) {
           float x[4];
           bool in[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) x[u] = i0 + u * kSampleThreads < n ? xs[i0 + u * kSampleThreads] : -INFINITY;
+          for (int u = 0; u < 4; ++u) x[u] = xs[i0 + u * kSampleThreads];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float b = bin_bits(x[u]);
-            in[u] = b >= from && b <= upto && x[u] > -INFINITY;
-          }
-          if (in[0] || in[1] || in[2] || in[3]) {  // seldom
+          for (int u = 0; u < 4; ++u) in[u] = x[u] >= lo_x && x[u] <= hi_x;
+          if (in[0] || in[1] || in[2] || in[3])  // seldom
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-              if (in[u]) {
-                const uint32_t at = atomicAdd(&sh.members, 1u);
-                if (at < kSampleList)
-                  sh.ord[at] = (static_cast<unsigned long long>(logit_key(x[u])) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id0 + i0 + u * kSampleThreads));
-              }
-          }
+              if (in[u]) take(x[u], i0 + u * kSampleThreads);
         }
+        for (; i0 < n; i0 += kSampleThreads) take(xs[i0], i0);
         __syncthreads();
         const int own = min(static_cast<int>(sh.members), kSampleList);
         if (t == 0 && own) sh.red[0] = atom_add_dsmem(mapa_shared(smem_u32(&sh.n_list), 0), static_cast<uint32_t>(own));
