@@ -21,13 +21,16 @@
 // shared memory of a cluster of CTAs.  A histogram of their distance from the
 // maximum (counts, merged through distributed shared memory) bounds the
 // tokens that can be kept; where they are few (1024: nearly always), they are
-// gathered in id order in one CTA, which finishes the row alone -- a cluster
-// barrier costs about a microsecond, a block's barrier a twentieth.  Else the
+// gathered in one CTA, which finishes the row alone -- a cluster barrier costs
+// about a microsecond, a block's barrier a twentieth -- and compares up to 256
+// of them with each other at once: five barriers instead of some twenty.  Else the
 // thresholds are found by 11-bit digits of the ordered key over the cluster.
-// 32 rows of 151,936 take 9 us greedy, 25 with min-p or nothing, 27 with top-k
-// 50 and 41 to 51 with top-p (four shared-memory atomics a token); one row of
-// 32,000 with both 18.6.  A single CTA a row with float64 weights took 4090 us
-// for 32 rows of mixed settings, this 51.
+// 32 rows of 151,936 take 9 us greedy, 25 with min-p or nothing, 23 with top-k
+// 50 and 39 to 48 with top-p (four shared-memory atomics a token); one row of
+// 32,000 with both 17.  A single CTA a row with float64 weights took 4090 us
+// for 32 rows of mixed settings, this 49.  Rows streamed from L2 by two or three
+// CTAs of 512 threads per SM instead of kept were slower at every size (32 rows
+// with top-k 38 us, 205 rows 162 and 138 against 135 then).
 #pragma once
 
 #include "cluster_mem.cuh"

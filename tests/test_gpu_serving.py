@@ -660,6 +660,20 @@ def test_sampling_follows_the_distribution_and_repeats_in_a_graph():
     assert torch.equal(tok, first)
 
 
+@pytest.mark.parametrize("tie", [1, 3])
+@pytest.mark.parametrize("extra", [dict(), dict(p=0.8), dict(m=0.02), dict(p=0.95, m=0.001)])
+def test_sampling_candidates_of_every_number(extra, tie):
+    """Lists of candidates around the sizes at which they are dealt out otherwise; alone and in threes of equal logits."""
+    B = require_gpu()
+    k = [1, 2, 31, 32, 33, 64, 65, 128, 129, 255, 256, 257, 300, 1023, 1024, 1025]
+    rows, vocab = len(k), 5003
+    ids = torch.randperm(vocab, device="cuda", generator=torch.Generator("cuda").manual_seed(2))
+    x = torch.empty(vocab, device="cuda")
+    x[ids] = -0.05 * torch.div(torch.arange(vocab, device="cuda"), tie, rounding_mode="floor").float()
+    for seed, T in ((1, 1.0), (2, 7.0)):
+        check_sample(B, x.expand(rows, vocab).contiguous(), uniforms(rows, seed), T=T, k=k, **extra)
+
+
 @pytest.mark.parametrize("rows", [1, 40])
 @pytest.mark.parametrize("filters", [dict(), dict(k=7), dict(p=1 - 2.0 ** -24)])
 def test_log_probability_of_a_token_alone_or_nearly(rows, filters):
